@@ -175,6 +175,17 @@ def _dequant(w, e):
     return (v * s.unsqueeze(-1)).view(n, rows, cols)
 
 
+def _moe_plain_part(st, x, ids, w):
+    T, k = ids.shape
+    xp = x.repeat_interleave(k, 0).unsqueeze(-1)
+    gu = torch.matmul(_dequant(st["gate_up"], ids.reshape(-1)), xp)  # [T k, 2I, 1], gate and up in chunks of 64
+    gu = gu.view(T * k, -1, 2, 64)
+    gate, up = gu[:, :, 0].reshape(T * k, -1), gu[:, :, 1].reshape(T * k, -1)
+    h = gate / (1.0 + torch.exp(-gate)) * up
+    y = torch.matmul(_dequant(st["down"], ids.reshape(-1)), h.unsqueeze(-1)).view(T, k, -1)
+    return (w.unsqueeze(-1) * y).sum(1)
+
+
 def _moe_plain(st):
     x, logits, k = st["x"], st["logits"], st["k"]
     T, H = x.shape
@@ -182,15 +193,9 @@ def _moe_plain(st):
     ids = order.indices[:, :k]
     p = torch.exp(order.values[:, :k] - order.values[:, :1])
     w = p / p.sum(-1, keepdim=True)
-    out = torch.empty(T, H, device="cuda")
-    for t in range(T):
-        xt = x[t].float()
-        gu = torch.matmul(_dequant(st["gate_up"], ids[t]), xt)  # [k, 2I], gate and up in chunks of 64
-        gu = gu.view(k, -1, 2, 64)
-        gate, up = gu[:, :, 0].reshape(k, -1), gu[:, :, 1].reshape(k, -1)
-        h = gate / (1.0 + torch.exp(-gate)) * up
-        y = torch.matmul(_dequant(st["down"], ids[t]), h.unsqueeze(-1)).squeeze(-1)
-        out[t] = (w[t].unsqueeze(-1) * y).sum(0)
+    # every (token, expert) pair's weights at once, in as few parts as their memory allows
+    n = max(1, (1 << 28) // (k * st["gate_up"][3] * H))
+    out = torch.cat([_moe_plain_part(st, x[t:t + n].float(), ids[t:t + n], w[t:t + n]) for t in range(0, T, n)])
     return {"out": out.bfloat16(), "ids": ids.int(), "weights": w}
 
 
