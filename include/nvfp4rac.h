@@ -466,6 +466,66 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
                                           void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* moe_w4a16_layer -- a whole MoE layer for a few tokens (T <= 64) in two kernels: routing,    */
+/* gate_up with SwiGLU, down and the weighted combine.  Activations stay bf16: at a few tokens */
+/* the layer is bound by the bytes of the touched experts' weights, so that nothing is gained  */
+/* by quantising them, no residual is needed (W_sel is not read), and the function is the      */
+/* trainer's own ("Two fixes": Asymmetric QAT quantises the weights only).                     */
+/*   (ids, w)_t as moe_route_topk;  h = silu(G x) * (U x);  out_t = bf16(sum_j w_tj D h_tj)     */
+/*   with the packed weights' values e * S * s_g; binary32 sums, one rounding at the end, h held */
+/*   with 11 significant bits or more.  The result does not depend on timing.                   */
+/*   x           bf16 [T x H], pitch ldx (>= H, a multiple of 8), 16-byte aligned.              */
+/*   logits      float32 [T x E], contiguous.  A token with an infinity or NaN among them gets   */
+/*               ids -1, weights 0 and a zero row, and NVFP4_ERR_RANGE goes to *dev_status.      */
+/*   w_gate_up   pack_weights with gate_up_interleave = 1: slabs E, rows = 2 I, cols = H.        */
+/*   w_down      pack_weights: slabs E, rows = H, cols = I.  NVFP4_SF_ATOM128, no row padding;  */
+/*               H % 128 == 0, I % 64 == 0, both <= 32768; E <= 1024, k <= min(32, E).           */
+/*   topk_ids    int32 [T x k], topk_w float32 [T x k]: the routing, as moe_route_topk gives it. */
+/*   out         bf16 [T x H], pitch ldo (>= H, a multiple of 8), 16-byte aligned.  May not      */
+/*               overlap x.                                                                      */
+/*   workspace   >= moe_w4a16_workspace_size() bytes, 16-byte aligned; nothing in it outlives    */
+/*               the call.  dev_status may be NULL.                                              */
+/* An infinity or NaN in x reaches the outputs of its token by the usual arithmetic.            */
+/* ---------------------------------------------------------------------------------------- */
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t I);
+nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
+                             const nvfp4_tensor* w_gate_up, const nvfp4_tensor* w_down, int32_t* topk_ids,
+                             float* topk_w, uint16_t* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* token_logprobs -- log probabilities of given tokens under softmax(logits / temperature),    */
+/* with the entropy of the distribution and its top alternatives: both sides of the            */
+/* rollout-trainer log-prob gap ("What it buys") in one pass over the logits.                   */
+/*   logits      [T x V] of type dtype (float32 or bf16), pitch ldl >= V elements, any alignment */
+/*               of elements.  -inf is a masked token.                                           */
+/*   ids         [T] int32 (id_bytes 4) or int64 (8).  id < 0 marks a padding row, which is not   */
+/*               read: logprob and entropy 0, top_ids -1, top_logprob 0, gradient 0.  id >= V is  */
+/*               NVFP4_ERR_INVALID_ARG in *dev_status and the row is treated as padding.          */
+/*   inv_temperature  1 / temperature, in (0, 1e30].                                             */
+/*   logprob     float32 [T]; entropy optional float32 [T], in nats.                              */
+/*   stats       optional float32 [T x 4], 16-byte aligned: what the backward call needs.         */
+/*   k_top       alternatives per row, 0 .. min(32, V): top_ids int32 [T x k_top] by logit        */
+/*               descending, ties to the lower index; top_logprob float32 [T x k_top].            */
+/*   A row of -inf only has no distribution: logprob and top_logprob -inf, entropy 0, gradient 0. */
+/*   A row with NaN or +inf gives NaN, and NVFP4_ERR_RANGE in *dev_status (which may be NULL).    */
+/* token_logprobs_backward -- with p = softmax(logits / temperature):                            */
+/*   grad_logits_v = inv_temperature * (grad_logprob * (1[v = id] - p_v)                          */
+/*                                      - grad_entropy * p_v * (ln p_v + entropy))                */
+/*   logits, ids, inv_temperature as in the forward call, stats from it; grad_logprob and         */
+/*   grad_entropy optional float32 [T] (NULL: zeros); grad_logits of the logits' type, pitch ldg  */
+/*   >= V: every row is written.  grad_logits == logits with ldg == ldl works in place; other     */
+/*   overlaps are not allowed.                                                                    */
+/* ---------------------------------------------------------------------------------------- */
+nvfp4_status token_logprobs(const void* logits, nvfp4_dtype dtype, int64_t T, int64_t V, int64_t ldl, const void* ids,
+                            int32_t id_bytes, float inv_temperature, int32_t k_top, float* logprob, float* entropy,
+                            float* stats, int32_t* top_ids, float* top_logprob, int32_t* dev_status, void* stream);
+nvfp4_status token_logprobs_backward(const void* logits, nvfp4_dtype dtype, int64_t T, int64_t V, int64_t ldl,
+                                     const void* ids, int32_t id_bytes, float inv_temperature, const float* stats,
+                                     const float* grad_logprob, const float* grad_entropy, void* grad_logits,
+                                     int64_t ldg, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------------- */
 /* weight_qdq -- trainer-side Asymmetric QAT fake quantisation of weights only (Two fixes):  */
 /* w_out = bf16(DQ(Q(w))) with one s_g per tensor; activations are not touched.  The         */
 /* quantiser is the one pack_weights uses, so DQ(pack_weights(W)) == weight_qdq(W) bitwise.  */

@@ -1167,6 +1167,129 @@ nvfp4_status moe_combine(const uint16_t* y, int64_t ldy, int64_t y_rows, const i
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "combine launch");
 }
 
+// ------------------------------------------------------------------------------------------ few-token layer
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t I) {
+  if (T <= 0 || k <= 0 || E <= 0 || I <= 0) return 0;
+  return round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256) +
+         round_up(moe_few_list_words(T, k, E) * sizeof(int32_t), 256);
+}
+
+nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
+                             const nvfp4_tensor* w_gate_up, const nvfp4_tensor* w_down, int32_t* topk_ids,
+                             float* topk_w, uint16_t* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  g_last_error.clear();
+  if (!w_gate_up || !w_down) return fail(NVFP4_ERR_INVALID_ARG, "w_gate_up / w_down is NULL");
+  const int64_t E = w_gate_up->slabs, H = w_gate_up->cols, I = w_down->cols;
+  if (T < 0 || T > kFewMaxTokens)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "T = %lld must be in [0, %d]", (long long)T, kFewMaxTokens);
+  if (E <= 0 || E > kMaxRouteExperts)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "E = %lld must be in [1, %d]", (long long)E, kMaxRouteExperts);
+  if (k <= 0 || k > 32 || k > E) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "k = %d must be in [1, min(32, E)]", k);
+  if (H <= 0 || H % 128 != 0 || H > kMaxK || I <= 0 || I % 64 != 0 || I > kMaxK)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H = %lld must be a multiple of 128, I = %lld of 64, both at most %lld",
+                (long long)H, (long long)I, (long long)kMaxK);
+  nvfp4_status st = check_tensor(w_gate_up, "w_gate_up", H, 2 * I, E);
+  if (st != NVFP4_OK) return st;
+  st = check_tensor(w_down, "w_down", I, H, E);
+  if (st != NVFP4_OK) return st;
+  if (w_gate_up->rows != 2 * I || w_gate_up->rows_padded != 2 * I || w_down->rows != H || w_down->rows_padded != H)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "w_gate_up needs 2 I = %lld rows and w_down H = %lld, without padding",
+                (long long)(2 * I), (long long)H);
+  if (T == 0) return NVFP4_OK;
+  if (!x || !logits || !topk_ids || !topk_w || !out) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  if (ldx < H || ldx % 8 != 0 || !aligned16(x))
+    return fail(NVFP4_ERR_ALIGNMENT, "x must be 16-byte aligned with a pitch >= H, a multiple of 8");
+  if (ldo < H || ldo % 8 != 0 || !aligned16(out))
+    return fail(NVFP4_ERR_ALIGNMENT, "out must be 16-byte aligned with a pitch >= H, a multiple of 8");
+  if (!workspace || workspace_bytes < moe_w4a16_workspace_size(T, k, (int32_t)E, I))
+    return fail(NVFP4_ERR_INVALID_ARG, "workspace too small");
+  if (!aligned16(workspace)) return fail(NVFP4_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  MoeFewArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.logits = logits;
+  a.T = (int32_t)T;
+  a.E = (int32_t)E;
+  a.k = k;
+  a.H = (int32_t)H;
+  a.I = (int32_t)I;
+  a.gu_codes = w_gate_up->codes;
+  a.gu_sf = w_gate_up->sf;
+  a.gu_sg = w_gate_up->s_g;
+  a.dn_codes = w_down->codes;
+  a.dn_sf = w_down->sf;
+  a.dn_sg = w_down->s_g;
+  a.ids = topk_ids;
+  a.topk_w = topk_w;
+  a.out = out;
+  a.ldo = ldo;
+  a.h = reinterpret_cast<float*>(workspace);
+  a.lists = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) +
+                                       round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256));
+  a.status = dev_status;
+  cudaError_t e = launch_moe_few(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "few-token layer launch");
+}
+
+// ------------------------------------------------------------------------------------------ log probabilities
+namespace {
+nvfp4_status check_logprobs(const void* logits, nvfp4_dtype dtype, int64_t T, int64_t V, int64_t ldl, const void* ids,
+                            int32_t id_bytes, float inv_temperature) {
+  if (dtype != NVFP4_OUT_F32 && dtype != NVFP4_OUT_BF16) return fail(NVFP4_ERR_INVALID_ARG, "bad logits type");
+  if (id_bytes != 4 && id_bytes != 8) return fail(NVFP4_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
+  if (T < 0 || T > INT32_MAX || V <= 0 || V > INT32_MAX)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "0 <= T, 0 < V required, both at most INT32_MAX");
+  if (!(inv_temperature > 0.0f) || !(inv_temperature <= 1e30f))
+    return fail(NVFP4_ERR_INVALID_ARG, "inv_temperature must be positive and at most 1e30");
+  if (T == 0) return NVFP4_OK;
+  if (!logits || !ids) return fail(NVFP4_ERR_INVALID_ARG, "logits / ids is NULL");
+  const uintptr_t esz = dtype == NVFP4_OUT_F32 ? 4 : 2;
+  if (ldl < V) return fail(NVFP4_ERR_ALIGNMENT, "ldl must be >= V");
+  if (reinterpret_cast<uintptr_t>(logits) % esz != 0 || reinterpret_cast<uintptr_t>(ids) % (uintptr_t)id_bytes != 0)
+    return fail(NVFP4_ERR_ALIGNMENT, "logits / ids must be aligned to their elements");
+  return NVFP4_OK;
+}
+}  // namespace
+
+nvfp4_status token_logprobs(const void* logits, nvfp4_dtype dtype, int64_t T, int64_t V, int64_t ldl, const void* ids,
+                            int32_t id_bytes, float inv_temperature, int32_t k_top, float* logprob, float* entropy,
+                            float* stats, int32_t* top_ids, float* top_logprob, int32_t* dev_status, void* stream) {
+  g_last_error.clear();
+  nvfp4_status st = check_logprobs(logits, dtype, T, V, ldl, ids, id_bytes, inv_temperature);
+  if (st != NVFP4_OK) return st;
+  if (k_top < 0 || k_top > 32 || k_top > V)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "k_top = %d must be in [0, min(32, V)]", k_top);
+  if (T == 0) return NVFP4_OK;
+  if (!logprob || (k_top > 0 && (!top_ids || !top_logprob))) return fail(NVFP4_ERR_INVALID_ARG, "NULL output buffer");
+  if (stats && !aligned16(stats)) return fail(NVFP4_ERR_ALIGNMENT, "stats must be 16-byte aligned");
+  LogprobArgs a{logits, T, V, ldl, dtype == NVFP4_OUT_BF16, ids, id_bytes, inv_temperature, k_top, logprob, entropy,
+                stats, top_ids, top_logprob, dev_status};
+  cudaError_t e = launch_logprobs(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "log probability launch");
+}
+
+nvfp4_status token_logprobs_backward(const void* logits, nvfp4_dtype dtype, int64_t T, int64_t V, int64_t ldl,
+                                     const void* ids, int32_t id_bytes, float inv_temperature, const float* stats,
+                                     const float* grad_logprob, const float* grad_entropy, void* grad_logits,
+                                     int64_t ldg, int32_t* dev_status, void* stream) {
+  g_last_error.clear();
+  nvfp4_status st = check_logprobs(logits, dtype, T, V, ldl, ids, id_bytes, inv_temperature);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (!stats || !grad_logits) return fail(NVFP4_ERR_INVALID_ARG, "stats / grad_logits is NULL");
+  if (!aligned16(stats)) return fail(NVFP4_ERR_ALIGNMENT, "stats must be 16-byte aligned");
+  const uintptr_t esz = dtype == NVFP4_OUT_F32 ? 4 : 2;
+  if (ldg < V || reinterpret_cast<uintptr_t>(grad_logits) % esz != 0)
+    return fail(NVFP4_ERR_ALIGNMENT, "grad_logits must be aligned to its elements, with ldg >= V");
+  if (grad_logits == logits && ldg != ldl)
+    return fail(NVFP4_ERR_INVALID_ARG, "in place needs ldg == ldl");
+  LogprobBwdArgs a{logits, T, V, ldl, dtype == NVFP4_OUT_BF16, ids, id_bytes, inv_temperature, stats, grad_logprob,
+                   grad_entropy, grad_logits, ldg, dev_status};
+  cudaError_t e = launch_logprobs_backward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "log probability backward launch");
+}
+
 // ------------------------------------------------------------------------------------------ qdq
 size_t weight_qdq_workspace_size(int64_t n_tensors, int64_t elems_per_tensor) {
   (void)elems_per_tensor;

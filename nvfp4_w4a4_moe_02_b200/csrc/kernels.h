@@ -229,6 +229,59 @@ cudaError_t launch_combine(const uint16_t* y, int64_t ldy, int64_t y_rows, const
                            int64_t T, int k, int64_t H, uint16_t* out, int64_t ldo, int num_sms, int32_t* status,
                            cudaStream_t st);
 
+// ---- whole MoE layer for a few tokens (csrc/moe_few.cu): bf16 activations on the packed weights
+constexpr int kFewMaxTokens = 64;
+constexpr int kFewMaxPairs = kFewMaxTokens * 32;
+struct MoeFewArgs {
+  const uint16_t* x;           // bf16 [T x H], pitch ldx
+  int64_t ldx;
+  const float* logits;         // [T x E]
+  int32_t T, E, k, H, I;
+  const uint8_t *gu_codes, *gu_sf, *dn_codes, *dn_sf;
+  const float *gu_sg, *dn_sg;  // [E]
+  int32_t* ids;                // [T x k]
+  float* topk_w;               // [T x k]
+  uint16_t* out;               // bf16 [T x H], pitch ldo
+  int64_t ldo;
+  float* h;                    // workspace: [T k x I] SwiGLU outputs, rows in expert order
+  int32_t* lists;              // workspace: moe_few_list_words(T, k, E) words
+  int32_t* status;
+};
+size_t moe_few_list_words(int64_t T, int32_t k, int32_t E);
+cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st);
+
+// ---- token log probabilities (csrc/logprobs.cu)
+struct LogprobArgs {
+  const void* logits;          // [T x V], pitch ld elements: bf16 or binary32
+  int64_t T, V, ld;
+  int32_t bf16;
+  const void* ids;             // [T], id_bytes 4 or 8; < 0: padding row
+  int32_t id_bytes;
+  float inv_temp;
+  int32_t k_top;
+  float* logprob;              // [T]
+  float* entropy;              // optional [T]
+  float* stats;                // optional [T x 4]: max logit, log2 of the sum, entropy
+  int32_t* top_ids;            // [T x k_top]
+  float* top_lp;               // [T x k_top]
+  int32_t* status;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t st);
+struct LogprobBwdArgs {
+  const void* logits;
+  int64_t T, V, ld;
+  int32_t bf16;
+  const void* ids;
+  int32_t id_bytes;
+  float inv_temp;
+  const float* stats;          // [T x 4]
+  const float *g_lp, *g_ent;   // optional [T]
+  void* grad;                  // [T x V], pitch ldg, the logits' type; may be the logits themselves
+  int64_t ldg;
+  int32_t* status;
+};
+cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st);
+
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int32_t* status, cudaStream_t st);
 
 }  // namespace nvfp4

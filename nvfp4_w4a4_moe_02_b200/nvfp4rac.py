@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -106,6 +107,12 @@ def load() -> ctypes.CDLL:
         "moe_row_pairs": ([vp, i64, i32, i64, vp, vp, vp], ctypes.c_int),
         "grouped_w4a4_rac_moe_combine": ([tp, tp, vp, vp, i32, tp, tp, i64, i64, i32, vp, vp, i64, i32, vp, vp, i64,
                                           vp, vp], ctypes.c_int),
+        "moe_w4a16_workspace_size": ([i64, i32, i32, i64], sz),
+        "moe_w4a16_layer": ([vp, i64, i64, vp, i32, tp, tp, vp, vp, vp, i64, vp, sz, vp, vp], ctypes.c_int),
+        "token_logprobs": ([vp, ctypes.c_int, i64, i64, i64, vp, i32, ctypes.c_float, i32, vp, vp, vp, vp, vp, vp, vp],
+                           ctypes.c_int),
+        "token_logprobs_backward": ([vp, ctypes.c_int, i64, i64, i64, vp, i32, ctypes.c_float, vp, vp, vp, vp, i64, vp,
+                                     vp], ctypes.c_int),
         "weight_qdq_workspace_size": ([i64, i64], sz),
         "weight_qdq": ([vp, i64, i64, vp, vp, vp, sz, vp, vp], ctypes.c_int),
         "weight_qdq_backward": ([vp, i64, vp, vp, vp], ctypes.c_int),
@@ -664,6 +671,179 @@ def grouped_w4a4_rac_moe_combine(a: Packed, a_res: Packed | None, expert_offsets
                                             topk_w.data_ptr(), T, k, out32.data_ptr(), out.data_ptr(), out.stride(0),
                                             st.data_ptr(), _stream(stream)))
     return out
+
+
+class _On:
+    """Makes the tensors' device current and `stream` (None: that device's current stream) the one
+    that buffers are allocated on and kernels are launched on."""
+
+    def __init__(self, device: torch.device, stream=None):
+        self.ctx = None
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self) -> int:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _arg(ok, text: str):
+    if not ok:
+        raise NVFP4Error(1, text)
+
+
+def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Packed, w_down: Packed,
+                    ids: torch.Tensor | None = None, w: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """A whole MoE layer for up to 64 tokens: bf16 x [T, H] and float32 router logits [T, E] ->
+    (out bf16 [T, H], ids int32 [T, k], weights float32 [T, k]).
+
+    Weights as the other paths use them: w_gate_up from pack_weights(gate_up_interleave=True)
+    [E, 2I, H], w_down from pack_weights [E, H, I].  Activations are not quantised: the layer is the
+    trainer's function of fake-quantised weights.  `workspace` (uint8, moe_w4a16_workspace_size
+    bytes) is allocated per call unless given; calls that may overlap need their own."""
+    lib = load()
+    _arg(x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.stride(1) == 1,
+         "x must be a bf16 CUDA matrix with unit column stride")
+    T, H = x.shape
+    E, I = w_gate_up.slabs, w_down.cols
+    dev = x.device
+    _arg(logits.shape == (T, E) and logits.dtype == torch.float32 and logits.is_contiguous() and logits.device == dev,
+         "logits must be contiguous float32 [T, E] on x's device")
+    _arg(w_gate_up.cols == H and w_down.slabs == E, "w_gate_up / w_down do not fit x and each other")
+    _arg(w_gate_up.codes.device == dev and w_down.codes.device == dev, "the weights must be on x's device")
+    for t, dtype, name in ((ids, torch.int32, "ids"), (w, torch.float32, "w")):
+        _arg(t is None or (t.shape == (T, k) and t.dtype == dtype and t.is_contiguous() and t.device == dev),
+             f"{name} must be a contiguous {dtype} [T, k] on x's device")
+    _arg(out is None or (out.shape == (T, H) and out.dtype == torch.bfloat16 and out.stride(1) == 1
+                         and out.device == dev), "out must be bf16 [T, H] with unit column stride on x's device")
+    _arg(workspace is None or (workspace.is_contiguous() and workspace.device == dev),
+         "workspace must be contiguous on x's device")
+    _arg(status is None or (status.dtype == torch.int32 and status.device == dev), "status must be int32 on x's device")
+    with _On(dev, stream) as s:
+        ids = torch.empty(T, k, dtype=torch.int32, device=dev) if ids is None else ids
+        w = torch.empty(T, k, dtype=torch.float32, device=dev) if w is None else w
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+        if workspace is None:
+            workspace = torch.empty(lib.moe_w4a16_workspace_size(T, k, E, I), dtype=torch.uint8, device=dev)
+        gu, dn = w_gate_up.c(), w_down.c()
+        _check(lib.moe_w4a16_layer(x.data_ptr(), T, x.stride(0) if T > 1 else H, logits.data_ptr(), k,
+                                   ctypes.byref(gu), ctypes.byref(dn), ids.data_ptr(), w.data_ptr(), out.data_ptr(),
+                                   out.stride(0) if T > 1 else H, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _ptr(status), s))
+    return out, ids, w
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: torch.Tensor                # float32 [T]
+    entropy: torch.Tensor                # float32 [T]
+    top_ids: torch.Tensor | None         # int32 [T, top]
+    top_logprobs: torch.Tensor | None    # float32 [T, top]
+
+
+def _logits_args(logits: torch.Tensor, ids: torch.Tensor, temperature: float):
+    _arg(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16),
+         "logits must be a float32 or bf16 CUDA matrix")
+    T, V = logits.shape
+    _arg(V == 1 or logits.stride(1) == 1, "logits must have unit column stride")
+    _arg(T <= 1 or logits.stride(0) >= V, "logits must have rows that do not overlap")
+    _arg(ids.shape == (T,) and ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous()
+         and ids.device == logits.device, "ids must be contiguous int32 or int64 [T] on the logits' device")
+    _arg(temperature > 0, "temperature must be positive")
+    dtype = OUT_F32 if logits.dtype == torch.float32 else OUT_BF16
+    return (logits.data_ptr(), dtype, T, V, logits.stride(0) if T > 1 else V, ids.data_ptr(), ids.element_size(),
+            1.0 / temperature)
+
+
+def _logprobs_forward(logits, ids, temperature, top, status, stream, want_stats):
+    args = _logits_args(logits, ids, temperature)
+    T, V = logits.shape
+    dev = logits.device
+    _arg(isinstance(top, int) and 0 <= top <= min(32, V), "top must be in [0, min(32, V)]")
+    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
+         "status must be int32 on the logits' device")
+    with _On(dev, stream) as s:
+        logprob, entropy = torch.empty(2, T, dtype=torch.float32, device=dev).unbind(0)
+        stats = torch.empty(T, 4, dtype=torch.float32, device=dev) if want_stats else None
+        top_ids = torch.empty(T, top, dtype=torch.int32, device=dev) if top else None
+        top_lp = torch.empty(T, top, dtype=torch.float32, device=dev) if top else None
+        _check(load().token_logprobs(*args, top, logprob.data_ptr(), entropy.data_ptr(), _ptr(stats), _ptr(top_ids),
+                                     _ptr(top_lp), _ptr(status), s))
+    return logprob, entropy, stats, top_ids, top_lp
+
+
+def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torch.Tensor, temperature: float = 1.0,
+                            grad_logprob: torch.Tensor | None = None, grad_entropy: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """dL/dlogits from dL/dlogprob and dL/dentropy (float32 [T], None: zeros) and the `stats` of
+    token_logprobs_forward; out may be the logits themselves."""
+    args = _logits_args(logits, ids, temperature)
+    T, V = logits.shape
+    dev = logits.device
+    _arg(stats.shape == (T, 4) and stats.dtype == torch.float32 and stats.is_contiguous() and stats.device == dev,
+         "stats must be the forward call's float32 [T, 4]")
+    for g in (grad_logprob, grad_entropy):
+        _arg(g is None or (g.shape == (T,) and g.dtype == torch.float32 and g.is_contiguous() and g.device == dev),
+             "row gradients must be contiguous float32 [T] on the logits' device")
+    _arg(out is None or (out.shape == (T, V) and out.dtype == logits.dtype and (V == 1 or out.stride(1) == 1)
+                         and (T <= 1 or out.stride(0) >= V) and out.device == dev),
+         "out must be a matrix like the logits")
+    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
+         "status must be int32 on the logits' device")
+    with _On(dev, stream) as s:
+        out = torch.empty(T, V, dtype=logits.dtype, device=dev) if out is None else out
+        _check(load().token_logprobs_backward(*args, stats.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
+                                              out.data_ptr(), out.stride(0) if T > 1 else V, _ptr(status), s))
+    return out
+
+
+def token_logprobs_forward(logits: torch.Tensor, ids: torch.Tensor, temperature: float = 1.0, top: int = 0,
+                           status: torch.Tensor | None = None, stream=None):
+    """token_logprobs without autograd -> (TokenLogprobs, stats); stats feeds token_logprobs_backward."""
+    lp, ent, stats, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, True)
+    return TokenLogprobs(lp, ent, ti, tl), stats
+
+
+class _TokenLogprobsFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, temperature, top, status, stream):
+        lp, ent, stats, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, True)
+        ctx.save_for_backward(logits, ids, stats)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in (ti, tl) if t is not None))
+        return lp, ent, ti, tl
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_lp, g_ent, *_):
+        logits, ids, stats = ctx.saved_tensors
+        g = [None if t is None else t.to(torch.float32).contiguous() for t in (g_lp, g_ent)]
+        return token_logprobs_backward(logits, ids, stats, ctx.temperature, *g), None, None, None, None, None
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float = 1.0, top: int = 0,
+                   status: torch.Tensor | None = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of the tokens ids [T] under softmax(logits / temperature), the entropies
+    and the `top` likeliest alternatives (logit descending, ties to the lower index).
+
+    logits: float32 or bf16 [T, V], any row pitch; -inf is a masked token.  ids: int32 or int64;
+    a negative id marks a padding row (zeros, top_ids -1, no gradient).  logprob and entropy carry
+    gradients to the logits."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_TokenLogprobsFn.apply(logits, ids, temperature, top, status, stream))
+    lp, ent, _, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, False)
+    return TokenLogprobs(lp, ent, ti, tl)
 
 
 def weight_qdq(w: torch.Tensor, out: torch.Tensor | None = None, s_g: torch.Tensor | None = None,
