@@ -41,12 +41,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {  // weights are read once
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -55,65 +49,93 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {  // weights are 
   return r;
 }
 
-// One 16 x 128 chunk of a tile as it is loaded: codes of the lane's two rows, one scale word.
+// One 16 x 128 chunk of a tile as it is loaded: 32 codes of each of the lane's two rows and the
+// scales of their two 16-blocks.
 struct Chunk {
   uint4 lo, hi;
-  uint32_t sf;
+  uint16_t sl, sh;
 };
 
 // The lane's part of a tile of a packed matrix.
 struct TileRef {
   const uint8_t* codes;  // the lane's low row, its 16 bytes of chunk 0
-  const uint8_t* sf;     // the lane's scale word of chunk 0
-  int64_t hi;            // bytes from the low row to the high row (64 rows)
+  const uint8_t* sf;     // the lane's two scales of the low row, chunk 0; the high row's follow 8 bytes on
 };
 
 __device__ __forceinline__ TileRef tile_ref(const uint8_t* codes, const uint8_t* sf, int tile, int cols) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int q = tile >> 3, jj = tile & 7;
-  const int64_t row = 128 * (int64_t)q + 32 * (g >> 2) + 4 * jj + (g & 3);
+  const int q = tile >> 3, jj = tile & 7, j = 4 * jj + (g & 3);
+  const int64_t row = 128 * (int64_t)q + 32 * (g >> 2) + j;
   TileRef r;
   r.codes = codes + row * (cols / 2) + 16 * t;
-  r.hi = 32 * (int64_t)cols;
-  r.sf = sf + ((int64_t)q * (cols / 64) + (lane >> 4)) * 512 + (4 * jj + ((lane >> 2) & 3)) * 16 + (lane & 3) * 4;
+  r.sf = sf + ((int64_t)q * (cols / 64) + (t >> 1)) * 512 + j * 16 + (g >> 2) * 4 + (t & 1) * 2;
   return r;
 }
 
-// A chunk past the last 64 columns reads zeros (scale 0).
-__device__ __forceinline__ Chunk load_chunk(const TileRef& r, int c, int cols) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint16_t ldg_u16(const uint8_t* p) {
+  uint16_t r;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+
+// hi: bytes from the low row to the high row (64 rows).  A chunk past the last 64 columns reads
+// zeros (scale 0).
+template <bool TAIL>
+__device__ __forceinline__ Chunk load_chunk(const TileRef& r, int64_t hi, int c, int cols) {
   Chunk k;
-  k.lo = k.hi = make_uint4(0, 0, 0, 0);
-  k.sf = 0;
-  if (128 * c + 32 * (lane & 3) < cols) {
-    k.lo = ldg_stream(r.codes + 64 * (int64_t)c);
-    k.hi = ldg_stream(r.codes + r.hi + 64 * (int64_t)c);
+  if (!TAIL || 128 * c + 32 * (int)(threadIdx.x & 3) < cols) {
+    const uint8_t* p = r.codes + 64 * (int64_t)c;
+    k.lo = ldg_stream(p);
+    k.hi = ldg_stream(p + hi);
+    k.sl = ldg_u16(r.sf + 1024 * (int64_t)c);
+    k.sh = ldg_u16(r.sf + 1024 * (int64_t)c + 8);
+  } else {
+    k.lo = k.hi = make_uint4(0, 0, 0, 0);
+    k.sl = k.sh = 0;
   }
-  if (128 * c + 64 * (lane >> 4) < cols) k.sf = __ldg(reinterpret_cast<const uint32_t*>(r.sf + 1024 * (int64_t)c));
   return k;
 }
 
+// The byte `i` of a word of codes -> two halves.  The conversion reads its register's low byte.
+template <int I>
+__device__ __forceinline__ uint32_t decode_byte(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.u8.u32 t, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(w >> (8 * I)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t scale_low(uint32_t a, __half2 s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __low2half2(s));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t scale_high(uint32_t a, __half2 s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(s));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ __half2 e4m3x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return *reinterpret_cast<const __half2*>(&r);
+}
+
 // acc += (chunk of weights) x (B fragments b of the same 128 elements), in units of the weights'
-// tensor scale and of the activations' chunk scale.
+// tensor scale and of the activations' scale.
 __device__ __forceinline__ void mma_chunk(float (&acc)[4], const Chunk& k, const uint32_t (&b)[16]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int src = (t >> 1) * 16 + (g & 3) * 4 + (g >> 2);
-  const uint32_t wl = __shfl_sync(0xffffffffu, k.sf, src), wh = __shfl_sync(0xffffffffu, k.sf, src + 2);
-  const uint16_t cl = (uint16_t)(wl >> (16 * (t & 1))), ch = (uint16_t)(wh >> (16 * (t & 1)));
-  uint32_t sl, sh;  // the scales of the lane's two 16-blocks, low and high row
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sl) : "h"(cl));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(ch));
-  const uint32_t s2[2][2] = {{__byte_perm(sl, sl, 0x1010), __byte_perm(sh, sh, 0x1010)},
-                             {__byte_perm(sl, sl, 0x3232), __byte_perm(sh, sh, 0x3232)}};
+  const __half2 sl = e4m3x2(k.sl), sh = e4m3x2(k.sh);
   const uint32_t lo[4] = {k.lo.x, k.lo.y, k.lo.z, k.lo.w}, hi[4] = {k.hi.x, k.hi.y, k.hi.z, k.hi.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int w = i >> 1, sh0 = 16 * (i & 1);
-    const uint32_t a0 = hmul2(e2m1x2_to_f16x2((lo[w] >> sh0) & 0xFFu), s2[w >> 1][0]);
-    const uint32_t a2 = hmul2(e2m1x2_to_f16x2((lo[w] >> (sh0 + 8)) & 0xFFu), s2[w >> 1][0]);
-    const uint32_t a1 = hmul2(e2m1x2_to_f16x2((hi[w] >> sh0) & 0xFFu), s2[w >> 1][1]);
-    const uint32_t a3 = hmul2(e2m1x2_to_f16x2((hi[w] >> (sh0 + 8)) & 0xFFu), s2[w >> 1][1]);
-    mma16816(acc, a0, a1, a2, a3, b[2 * i], b[2 * i + 1]);
+  for (int w = 0; w < 4; ++w) {
+    // a word is 8 codes: the first two words belong to the lane's first 16-block
+    auto sc = [&](uint32_t a, __half2 s) { return w < 2 ? scale_low(a, s) : scale_high(a, s); };
+    mma16816(acc, sc(decode_byte<0>(lo[w]), sl), sc(decode_byte<0>(hi[w]), sh), sc(decode_byte<1>(lo[w]), sl),
+             sc(decode_byte<1>(hi[w]), sh), b[4 * w], b[4 * w + 1]);
+    mma16816(acc, sc(decode_byte<2>(lo[w]), sl), sc(decode_byte<2>(hi[w]), sh), sc(decode_byte<3>(lo[w]), sl),
+             sc(decode_byte<3>(hi[w]), sh), b[4 * w + 2], b[4 * w + 3]);
   }
 }
 
@@ -353,7 +375,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) moe_few_gate_up_kernel(MoeFewA
       for (int c = warp; c < nch; c += kWarps) {
         Chunk ck[kTiles];
 #pragma unroll
-        for (int r = 0; r < kTiles; ++r) ck[r] = load_chunk(ref[r], c, a.H);
+        for (int r = 0; r < kTiles; ++r) ck[r] = load_chunk<false>(ref[r], 32 * (int64_t)a.H, c, a.H);
         uint32_t b[16];
         const float down = load_b_bf16(xr, has, c, a.H, b) * s_g;
         const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) moe_few_down_kernel(MoeFewAr
       for (int c = c0; c < c1; ++c) {
         Chunk ck[kDnTiles];
 #pragma unroll
-        for (int r = 0; r < kDnTiles; ++r) ck[r] = load_chunk(ref[r], c, a.I);
+        for (int r = 0; r < kDnTiles; ++r) ck[r] = load_chunk<true>(ref[r], 32 * (int64_t)a.I, c, a.I);
         uint32_t b[16];
         const float down = load_b_f32(hr, has, c, a.I, b) * s_g;
         const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
