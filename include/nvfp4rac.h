@@ -487,7 +487,7 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
 /*               the call.  dev_status may be NULL.                                              */
 /* An infinity or NaN in x reaches the outputs of its token by the usual arithmetic.            */
 /* ---------------------------------------------------------------------------------------- */
-size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t I);
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
                              const nvfp4_tensor* w_gate_up, const nvfp4_tensor* w_down, int32_t* topk_ids,
                              float* topk_w, uint16_t* out, int64_t ldo, void* workspace, size_t workspace_bytes,

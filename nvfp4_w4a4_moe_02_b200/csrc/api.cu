@@ -1168,10 +1168,14 @@ nvfp4_status moe_combine(const uint16_t* y, int64_t ldy, int64_t y_rows, const i
 }
 
 // ------------------------------------------------------------------------------------------ few-token layer
-size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t I) {
-  if (T <= 0 || k <= 0 || E <= 0 || I <= 0) return 0;
-  return round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256) +
-         round_up(moe_few_list_words(T, k, E) * sizeof(int32_t), 256);
+namespace {
+size_t few_h_bytes(int64_t T, int32_t k, int64_t I) { return round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256); }
+size_t few_partial_bytes(int64_t T) { return round_up(moe_few_partial_floats(T) * sizeof(float), 256); }
+}  // namespace
+
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
+  if (T <= 0 || T > kFewMaxTokens || k <= 0 || k > 32 || E <= 0 || H <= 0 || I <= 0) return 0;
+  return few_h_bytes(T, k, I) + few_partial_bytes(T) + round_up(moe_few_list_words(T, k, E, H) * sizeof(int32_t), 256);
 }
 
 nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
@@ -1202,7 +1206,7 @@ nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const fl
     return fail(NVFP4_ERR_ALIGNMENT, "x must be 16-byte aligned with a pitch >= H, a multiple of 8");
   if (ldo < H || ldo % 8 != 0 || !aligned16(out))
     return fail(NVFP4_ERR_ALIGNMENT, "out must be 16-byte aligned with a pitch >= H, a multiple of 8");
-  if (!workspace || workspace_bytes < moe_w4a16_workspace_size(T, k, (int32_t)E, I))
+  if (!workspace || workspace_bytes < moe_w4a16_workspace_size(T, k, (int32_t)E, H, I))
     return fail(NVFP4_ERR_INVALID_ARG, "workspace too small");
   if (!aligned16(workspace)) return fail(NVFP4_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   MoeFewArgs a;
@@ -1224,9 +1228,10 @@ nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const fl
   a.topk_w = topk_w;
   a.out = out;
   a.ldo = ldo;
-  a.h = reinterpret_cast<float*>(workspace);
-  a.lists = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) +
-                                       round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256));
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  a.h = reinterpret_cast<float*>(ws);
+  a.partial = reinterpret_cast<float*>(ws + few_h_bytes(T, k, I));
+  a.lists = reinterpret_cast<int32_t*>(ws + few_h_bytes(T, k, I) + few_partial_bytes(T));
   a.status = dev_status;
   cudaError_t e = launch_moe_few(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "few-token layer launch");

@@ -244,10 +244,12 @@ struct MoeFewArgs {
   uint16_t* out;               // bf16 [T x H], pitch ldo
   int64_t ldo;
   float* h;                    // workspace: [T k x I] SwiGLU outputs, rows in expert order
-  int32_t* lists;              // workspace: moe_few_list_words(T, k, E) words
+  float* partial;              // workspace: moe_few_partial_floats(T)
+  int32_t* lists;              // workspace: moe_few_list_words(T, k, E, H) words
   int32_t* status;
 };
-size_t moe_few_list_words(int64_t T, int32_t k, int32_t E);
+size_t moe_few_list_words(int64_t T, int32_t k, int32_t E, int64_t H);
+size_t moe_few_partial_floats(int64_t T);
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st);
 
 // ---- token log probabilities (csrc/logprobs.cu)

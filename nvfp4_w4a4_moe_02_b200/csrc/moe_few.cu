@@ -25,13 +25,17 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 4;       // warps of a gate_up block: they split K
-constexpr int kTiles = 4;       // 16-row tiles per gate_up block
-constexpr int kDnWarps = 8;     // warps of a down block: they split the (expert, K) list
-constexpr int kDnTiles = 2;
+constexpr int kTiles = 4;       // 16-row tiles per gate_up item
+constexpr int kDnWarps = 8;     // warps of a down block: they split the (slot, K) list
+constexpr int kDnTiles = 4;
+constexpr int kDnRows = 16 * kDnTiles;
 
-// workspace lists: [0] touched experts n, then (expert, first pair) x n, one closing (-, pairs),
-// then the pairs t * k + j in expert order
+// A slot is up to eight tokens (pairs) of one expert.  Workspace words: [0] slots n, then (expert,
+// first pair, end) x n from kListHead on, the pairs t * k + j in slot order, and one arrival count
+// per kDnRows output columns (zeroed by the gate_up kernel).
 constexpr int kListHead = 16;
+constexpr int kFewMaxSlots = kMaxRouteExperts + kFewMaxPairs / 8;
+__host__ __device__ inline int max_slots(int P, int E) { return P < E + P / 8 ? P : E + P / 8; }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -62,9 +66,10 @@ struct TileRef {
   const uint8_t* sf;     // the lane's two scales of the low row, chunk 0; the high row's follow 8 bytes on
 };
 
+// Of a tile whose index is a multiple of 4; the three after it lie 4 rows and 64 scale bytes apart.
 __device__ __forceinline__ TileRef tile_ref(const uint8_t* codes, const uint8_t* sf, int tile, int cols) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int q = tile >> 3, jj = tile & 7, j = 4 * jj + (g & 3);
+  const int q = tile >> 3, j = 4 * (tile & 7) + (g & 3);
   const int64_t row = 128 * (int64_t)q + 32 * (g >> 2) + j;
   TileRef r;
   r.codes = codes + row * (cols / 2) + 16 * t;
@@ -78,17 +83,15 @@ __device__ __forceinline__ uint16_t ldg_u16(const uint8_t* p) {
   return r;
 }
 
-// hi: bytes from the low row to the high row (64 rows).  A chunk past the last 64 columns reads
-// zeros (scale 0).
-template <bool TAIL>
-__device__ __forceinline__ Chunk load_chunk(const TileRef& r, int64_t hi, int c, int cols) {
+// Tile `r` after the reference; `in` false (past the last 64 columns): zeros.
+__device__ __forceinline__ Chunk load_chunk(const TileRef& ref, int r, int cols, bool in) {
   Chunk k;
-  if (!TAIL || 128 * c + 32 * (int)(threadIdx.x & 3) < cols) {
-    const uint8_t* p = r.codes + 64 * (int64_t)c;
+  if (in) {
+    const uint8_t* p = ref.codes + r * (2 * cols);
     k.lo = ldg_stream(p);
-    k.hi = ldg_stream(p + hi);
-    k.sl = ldg_u16(r.sf + 1024 * (int64_t)c);
-    k.sh = ldg_u16(r.sf + 1024 * (int64_t)c + 8);
+    k.hi = ldg_stream(p + 32 * (int64_t)cols);
+    k.sl = ldg_u16(ref.sf + 64 * r);
+    k.sh = ldg_u16(ref.sf + 64 * r + 8);
   } else {
     k.lo = k.hi = make_uint4(0, 0, 0, 0);
     k.sl = k.sh = 0;
@@ -156,26 +159,32 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+}
+
 // B fragments of 128 elements of the lane's column (token), and the scale taken out.
 __device__ __forceinline__ float scale_to_f16(const float (&v)[32], uint32_t (&b)[16]) {
-  float m = 0.0f;
+  float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < 32; i += 4) {
+    m0 = max3_abs(m0, v[i], v[i + 1]);
+    m1 = max3_abs(m1, v[i + 2], v[i + 3]);
+  }
   float up, down;
-  chunk_scale(quad_max(m), &up, &down);
+  chunk_scale(quad_max(fmaxf(m0, m1)), &up, &down);
 #pragma unroll
   for (int i = 0; i < 16; ++i) b[i] = pack_f16(v[2 * i] * up, v[2 * i + 1] * up);
   return down;
 }
 
-__device__ __forceinline__ float load_b_bf16(const uint16_t* row, bool has, int c, int cols, uint32_t (&b)[16]) {
-  const int t = threadIdx.x & 3;
+// row: the lane's 32 elements of the chunk; `in` false: zeros
+__device__ __forceinline__ float load_b_bf16(const uint16_t* row, bool in, uint32_t (&b)[16]) {
   float v[32];
-  const bool in = has && 128 * c + 32 * t < cols;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint4 r = make_uint4(0, 0, 0, 0);
-    if (in) r = __ldg(reinterpret_cast<const uint4*>(row + 128 * c + 32 * t) + i);
+    if (in) r = __ldg(reinterpret_cast<const uint4*>(row) + i);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -186,14 +195,12 @@ __device__ __forceinline__ float load_b_bf16(const uint16_t* row, bool has, int 
   return scale_to_f16(v, b);
 }
 
-__device__ __forceinline__ float load_b_f32(const float* row, bool has, int c, int cols, uint32_t (&b)[16]) {
-  const int t = threadIdx.x & 3;
+__device__ __forceinline__ float load_b_f32(const float* row, bool in, uint32_t (&b)[16]) {
   float v[32];
-  const bool in = has && 128 * c + 32 * t < cols;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (in) r = __ldg(reinterpret_cast<const float4*>(row + 128 * c + 32 * t) + i);
+    if (in) r = __ldg(reinterpret_cast<const float4*>(row) + i);
     v[4 * i] = r.x;
     v[4 * i + 1] = r.y;
     v[4 * i + 2] = r.z;
@@ -206,9 +213,10 @@ struct Lists {
   uint16_t id[kFewMaxPairs];             // expert of pair t * k + j (0xFFFF: none)
   uint16_t order[kFewMaxPairs];          // pairs in expert order, tokens ascending
   int cursor[kMaxRouteExperts];
-  uint16_t expert[kMaxRouteExperts];     // touched experts, ascending
-  uint16_t start[kMaxRouteExperts + 1];  // first pair of each
-  int n;
+  uint16_t expert[kFewMaxSlots];         // slots, experts ascending
+  uint16_t start[kFewMaxSlots];          // first pair of each
+  uint8_t count[kFewMaxSlots];
+  int n, pairs;
 };
 
 // The same choice and weights as moe_route_topk: k rounds of a warp arg-max over ordered keys.
@@ -292,29 +300,33 @@ __device__ void build_lists(const MoeFewArgs& a, Lists& L) {
     if (L.id[p] != 0xFFFFu) atomicAdd(&L.cursor[L.id[p]], 1);
   __syncthreads();
   if (warp == 0) {
-    int n = 0, at = 0;
+    int n = 0, at = 0;  // slots and pairs before this group of experts
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
       const int cnt = e < a.E ? L.cursor[e] : 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, cnt > 0);
-      int run = cnt;
+      if (__ballot_sync(0xffffffffu, cnt > 0) == 0) continue;
+      int run = cnt | (cnt + 7) / 8 << 16;  // pairs low, slots high
+      const int own = run;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += v;
       }
-      if (cnt > 0) {
-        const int i = n + __popc(m & ((1u << lane) - 1u));
+      const int first = at + ((run - own) & 0xFFFF);
+      int i = n + ((run - own) >> 16);
+      for (int c = 0; c < cnt; c += 8, ++i) {
         L.expert[i] = (uint16_t)e;
-        L.start[i] = (uint16_t)(at + run - cnt);
-        L.cursor[e] = at + run - cnt;
+        L.start[i] = (uint16_t)(first + c);
+        L.count[i] = (uint8_t)min(8, cnt - c);
       }
-      n += __popc(m);
-      at += __shfl_sync(0xffffffffu, run, 31);
+      if (cnt > 0) L.cursor[e] = first;
+      const int all = __shfl_sync(0xffffffffu, run, 31);
+      at += all & 0xFFFF;
+      n += all >> 16;
     }
     if (lane == 0) {
       L.n = n;
-      L.start[n] = (uint16_t)at;
+      L.pairs = at;
     }
     __syncwarp();
     // ranks in pair order, 32 at a time
@@ -338,131 +350,199 @@ __device__ void build_lists(const MoeFewArgs& a, Lists& L) {
     const int n = L.n;
     int32_t* o = a.lists;
     if (threadIdx.x == 0) o[0] = n;
-    for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-      o[kListHead + 2 * i] = i < n ? L.expert[i] : -1;
-      o[kListHead + 2 * i + 1] = L.start[i];
+    o += kListHead;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      o[3 * i] = L.expert[i];
+      o[3 * i + 1] = L.start[i];
+      o[3 * i + 2] = L.start[i] + L.count[i];
     }
-    int32_t* ord = o + kListHead + 2 * (min(P, a.E) + 1);
-    for (int p = threadIdx.x; p < L.start[n]; p += blockDim.x) ord[p] = L.order[p];
+    o += 3 * max_slots(P, a.E);
+    for (int p = threadIdx.x; p < L.pairs; p += blockDim.x) o[p] = L.order[p];
+    o += P;
+    for (int i = threadIdx.x; i < a.H / kDnRows; i += blockDim.x) o[i] = 0;
   }
 }
 
 }  // namespace
 
-// gate_up + SwiGLU.  An item is (touched expert, kTiles tiles); a block's warps split its K in
-// interleaved chunks and join their sums in shared memory, in warp order.
+// gate_up + SwiGLU.  An item is (slot, kTiles tiles); a block's warps split its K in interleaved
+// chunks and join their sums in shared memory, in warp order.  Each warp keeps the next chunk of
+// every tile in flight, across the end of an item too.
 __global__ void __launch_bounds__(kWarps * 32, 4) moe_few_gate_up_kernel(MoeFewArgs a) {
   __shared__ Lists L;
   __shared__ float red[kWarps][kTiles][16][8];
   build_lists(a, L);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int groups = a.I / 8 / kTiles;
-  const int nch = (a.H + 127) / 128;
+  const int nch = a.H / 128;
   const int items = L.n * groups;
   const int64_t cb = (int64_t)a.I * a.H, sb = (int64_t)a.I * a.H / 8;  // bytes of one expert's codes / scales
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const int ei = it / groups, grp = it % groups;
-    const int e = L.expert[ei];
-    const float s_g = __ldg(a.gu_sg + e);
-    TileRef ref[kTiles];
+  auto item_ref = [&](int it) {
+    const int64_t e = L.expert[it / groups];
+    TileRef r = tile_ref(a.gu_codes + e * cb, a.gu_sf + e * sb, it % groups * kTiles, a.H);
+    r.codes += 64 * warp;
+    r.sf += 1024 * warp;
+    return r;
+  };
+  int it = blockIdx.x;
+  if (it >= items) return;
+  TileRef next = item_ref(it);  // what the ring holds or is about to
+  Chunk ring[kTiles];
+  const bool any = warp < nch;
 #pragma unroll
-    for (int r = 0; r < kTiles; ++r) ref[r] = tile_ref(a.gu_codes + e * cb, a.gu_sf + e * sb, grp * kTiles + r, a.H);
-    for (int p0 = L.start[ei]; p0 < L.start[ei + 1]; p0 += 8) {
-      const int cnt = min(8, L.start[ei + 1] - p0);
-      const bool has = g < cnt;
-      const uint16_t* xr = a.x + (has ? (int64_t)(L.order[p0 + g] / a.k) * a.ldx : 0);
-      float acc[kTiles][4] = {};
-      for (int c = warp; c < nch; c += kWarps) {
-        Chunk ck[kTiles];
-#pragma unroll
-        for (int r = 0; r < kTiles; ++r) ck[r] = load_chunk<false>(ref[r], 32 * (int64_t)a.H, c, a.H);
-        uint32_t b[16];
-        const float down = load_b_bf16(xr, has, c, a.H, b) * s_g;
-        const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-        for (int r = 0; r < kTiles; ++r) {
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_chunk(part, ck[r], b);
-          acc[r][0] = fmaf(part[0], d0, acc[r][0]);
-          acc[r][1] = fmaf(part[1], d1, acc[r][1]);
-          acc[r][2] = fmaf(part[2], d0, acc[r][2]);
-          acc[r][3] = fmaf(part[3], d1, acc[r][3]);
-        }
+  for (int r = 0; r < kTiles; ++r) ring[r] = load_chunk(next, r, a.H, any);
+  for (; it < items; it += gridDim.x) {
+    const int slot = it / groups;
+    const int p0 = L.start[slot], cnt = L.count[slot];
+    const float s_g = __ldg(a.gu_sg + L.expert[slot]);
+    const bool has = g < cnt;
+    const uint16_t* xr = a.x + (has ? (int64_t)(L.order[p0 + g] / a.k) * a.ldx : 0) + 32 * t;
+    float acc[kTiles][4] = {};
+    for (int c = warp; c < nch; c += kWarps) {
+      bool more = true;
+      if (c + kWarps < nch) {
+        next.codes += 64 * kWarps;
+        next.sf += 1024 * kWarps;
+      } else if (it + gridDim.x < items) {
+        next = item_ref(it + gridDim.x);
+      } else {
+        more = false;
       }
+      uint32_t b[16];
+      const float down = load_b_bf16(xr + 128 * c, has, b) * s_g;
+      const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
       for (int r = 0; r < kTiles; ++r) {
-        *reinterpret_cast<float2*>(&red[warp][r][g][2 * t]) = make_float2(acc[r][0], acc[r][1]);
-        *reinterpret_cast<float2*>(&red[warp][r][g + 8][2 * t]) = make_float2(acc[r][2], acc[r][3]);
+        const Chunk k = ring[r];
+        if (more) ring[r] = load_chunk(next, r, a.H, true);
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_chunk(part, k, b);
+        acc[r][0] = fmaf(part[0], d0, acc[r][0]);
+        acc[r][1] = fmaf(part[1], d1, acc[r][1]);
+        acc[r][2] = fmaf(part[2], d0, acc[r][2]);
+        acc[r][3] = fmaf(part[3], d1, acc[r][3]);
       }
-      __syncthreads();
-      for (int o = threadIdx.x; o < kTiles * 64; o += kWarps * 32) {
-        const int col = o >> 5, r = (o >> 3) & 3, row = o & 7;
-        if (col < cnt) {
-          float gate = 0.0f, up = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            gate += red[w][r][row][col];
-            up += red[w][r][row + 8][col];
-          }
-          const int tile = grp * kTiles + r;
-          const int hi = 64 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
-          a.h[(int64_t)(p0 + col) * a.I + hi] = gate / (1.0f + expf(-gate)) * up;
-        }
-      }
-      __syncthreads();
     }
+#pragma unroll
+    for (int r = 0; r < kTiles; ++r) {
+      *reinterpret_cast<float2*>(&red[warp][r][g][2 * t]) = make_float2(acc[r][0], acc[r][1]);
+      *reinterpret_cast<float2*>(&red[warp][r][g + 8][2 * t]) = make_float2(acc[r][2], acc[r][3]);
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < kTiles * 64; o += kWarps * 32) {
+      const int col = o >> 5, r = (o >> 3) & 3, row = o & 7;
+      if (col < cnt) {
+        float gate = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          gate += red[w][r][row][col];
+          up += red[w][r][row + 8][col];
+        }
+        const int tile = it % groups * kTiles + r;
+        const int hi = 64 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
+        a.h[(int64_t)(p0 + col) * a.I + hi] = gate / (1.0f + expf(-gate)) * up;
+      }
+    }
+    __syncthreads();
   }
 }
 
-// down + combine.  A block owns kDnTiles tiles of output columns for all tokens; its warps take
-// equal stretches of the (touched expert, chunk) list, each adding w_tj * sum into a private
-// [T][rows] array; the arrays are summed in warp order, so the result does not depend on timing.
+// down + combine.  The units (kDnRows output columns, slot), columns outermost, are split evenly over
+// the blocks, so that few tokens still fill the card and many leave no last wave; a block's warps
+// split the (slot, chunk) list of each stretch, each adding w_tj * sum into a private [T][kDnRows]
+// array, joined in warp order.  Columns that several blocks share go through the workspace: the last
+// of these blocks to arrive adds their parts, in block order, so the result does not depend on timing.
 __global__ void __launch_bounds__(kDnWarps * 32, 2) moe_few_down_kernel(MoeFewArgs a) {
-  extern __shared__ float accw[];  // [kDnWarps][T][16 kDnTiles]
-  constexpr int kRows = 16 * kDnTiles;
+  extern __shared__ float accw[];  // [kDnWarps][T][kDnRows]
+  __shared__ int last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int P = a.T * a.k;
-  const int n = __ldg(a.lists);
+  const int n = a.lists[0];
   const int32_t* list = a.lists + kListHead;
-  const int32_t* order = list + 2 * (min(P, a.E) + 1);
+  const int32_t* order = list + 3 * max_slots(P, a.E);
+  int32_t* arrived = a.lists + kListHead + 3 * max_slots(P, a.E) + P;
   const int nch = (a.I + 127) / 128;
   const int64_t cb = (int64_t)a.H * a.I / 2, sb = (int64_t)a.H * a.I / 16;
-  float* mine = accw + warp * a.T * kRows;
-  for (int i = lane; i < a.T * kRows; i += 32) mine[i] = 0.0f;
-  __syncwarp();
-  const int units = n * nch;
-  int u = (int)((int64_t)units * warp / kDnWarps);
-  const int u_end = (int)((int64_t)units * (warp + 1) / kDnWarps);
-  while (u < u_end) {
-    const int ei = u / nch, c0 = u % nch;
-    const int c1 = min(nch, c0 + (u_end - u));
-    const int e = __ldg(list + 2 * ei);
-    const int s0 = __ldg(list + 2 * ei + 1), s1 = __ldg(list + 2 * ei + 3);
-    const float s_g = __ldg(a.dn_sg + e);
-    TileRef ref[kDnTiles];
+  const int elems = a.T * kDnRows;
+  const int groups = a.H / kDnRows;
+  auto store = [&](int grp, int i, float v) {
+    const int row = i % 16, tile = grp * kDnTiles + i % kDnRows / 16;
+    const int col = 128 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    a.out[(int64_t)(i / kDnRows) * a.ldo + col] = *reinterpret_cast<const uint16_t*>(&b);
+  };
+  if (n == 0) {  // no token could be routed
+    for (int grp = blockIdx.x; grp < groups; grp += gridDim.x)
+      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) store(grp, i, 0.0f);
+    return;
+  }
+  const int64_t units = (int64_t)groups * n;
+  const int64_t G = min((int64_t)gridDim.x, units);
+  if (blockIdx.x >= G) return;
+  auto bound = [&](int64_t b) { return units * b / G; };                       // first unit of block b
+  auto block_of = [&](int64_t u) { return ((u + 1) * G - 1) / units; };        // the block that holds unit u
+  int64_t u = bound(blockIdx.x);
+  const int64_t u_end = bound(blockIdx.x + 1);
+  float* mine = accw + warp * elems;
+  for (int part = 0; u < u_end; ++part) {
+    const int grp = (int)(u / n);
+    const int s_lo = (int)(u - (int64_t)grp * n);
+    const int s_hi = (int)min((int64_t)n, s_lo + (u_end - u));
+    u += s_hi - s_lo;
+    for (int i = lane; i < elems; i += 32) mine[i] = 0.0f;
+    __syncwarp();
+    const int todo = (s_hi - s_lo) * nch;
+    int w0 = todo * warp / kDnWarps;
+    const int w1 = todo * (warp + 1) / kDnWarps;
+    int slot = s_lo + w0 / nch, c = w0 % nch;
+    auto slot_ref = [&](int sl, int ch) {
+      const int64_t e = __ldg(list + 3 * sl);
+      TileRef r = tile_ref(a.dn_codes + e * cb, a.dn_sf + e * sb, grp * kDnTiles, a.I);
+      r.codes += 64 * ch;
+      r.sf += 1024 * ch;
+      return r;
+    };
+    TileRef next;
+    Chunk ring[kDnTiles];
+    if (w0 < w1) {
+      next = slot_ref(slot, c);
 #pragma unroll
-    for (int r = 0; r < kDnTiles; ++r)
-      ref[r] = tile_ref(a.dn_codes + e * cb, a.dn_sf + e * sb, blockIdx.x * kDnTiles + r, a.I);
-    for (int p0 = s0; p0 < s1; p0 += 8) {
-      const int cnt = min(8, s1 - p0);
+      for (int r = 0; r < kDnTiles; ++r) ring[r] = load_chunk(next, r, a.I, 128 * c + 32 * t < a.I);
+    }
+    while (w0 < w1) {
+      const int c_end = min(nch, c + (w1 - w0));
+      const int p0 = __ldg(list + 3 * slot + 1), cnt = __ldg(list + 3 * slot + 2) - p0;
+      const float s_g = __ldg(a.dn_sg + __ldg(list + 3 * slot));
       const bool has = g < cnt;
-      const float* hr = a.h + (int64_t)(has ? p0 + g : 0) * a.I;
+      const float* hr = a.h + (int64_t)(has ? p0 + g : 0) * a.I + 32 * t;
       float acc[kDnTiles][4] = {};
-      for (int c = c0; c < c1; ++c) {
-        Chunk ck[kDnTiles];
-#pragma unroll
-        for (int r = 0; r < kDnTiles; ++r) ck[r] = load_chunk<true>(ref[r], 32 * (int64_t)a.I, c, a.I);
+      w0 += c_end - c;
+      for (; c < c_end; ++c) {
+        bool more = true;
+        int cn = c + 1;
+        if (cn < c_end) {
+          next.codes += 64;
+          next.sf += 1024;
+        } else if (w0 < w1) {
+          next = slot_ref(slot + 1, 0);
+          cn = 0;
+        } else {
+          more = false;
+        }
+        const bool in = 128 * c + 32 * t < a.I, in_next = more && 128 * cn + 32 * t < a.I;
         uint32_t b[16];
-        const float down = load_b_f32(hr, has, c, a.I, b) * s_g;
+        const float down = load_b_f32(hr + 128 * c, has && in, b) * s_g;
         const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
         for (int r = 0; r < kDnTiles; ++r) {
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_chunk(part, ck[r], b);
-          acc[r][0] = fmaf(part[0], d0, acc[r][0]);
-          acc[r][1] = fmaf(part[1], d1, acc[r][1]);
-          acc[r][2] = fmaf(part[2], d0, acc[r][2]);
-          acc[r][3] = fmaf(part[3], d1, acc[r][3]);
+          const Chunk k = ring[r];
+          ring[r] = load_chunk(next, r, a.I, in_next);
+          float pt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_chunk(pt, k, b);
+          acc[r][0] = fmaf(pt[0], d0, acc[r][0]);
+          acc[r][1] = fmaf(pt[1], d1, acc[r][1]);
+          acc[r][2] = fmaf(pt[2], d0, acc[r][2]);
+          acc[r][3] = fmaf(pt[3], d1, acc[r][3]);
         }
       }
 #pragma unroll
@@ -471,47 +551,80 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) moe_few_down_kernel(MoeFewAr
         if (col < cnt) {
           const int p = __ldg(order + p0 + col);
           const float w = __ldg(a.topk_w + p);
-          float* o = mine + (p / a.k) * kRows;  // an expert's tokens are distinct: no two lanes meet
+          float* o = mine + (p / a.k) * kDnRows + g;  // a slot's tokens are distinct: no two lanes meet
 #pragma unroll
           for (int r = 0; r < kDnTiles; ++r) {
-            o[16 * r + g] = fmaf(w, acc[r][j], o[16 * r + g]);
-            o[16 * r + g + 8] = fmaf(w, acc[r][2 + j], o[16 * r + g + 8]);
+            o[16 * r] = fmaf(w, acc[r][j], o[16 * r]);
+            o[16 * r + 8] = fmaf(w, acc[r][2 + j], o[16 * r + 8]);
           }
         }
       }
       __syncwarp();
+      ++slot;
+      c = 0;
     }
-    u += c1 - c0;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * kRows; i += kDnWarps * 32) {
-    float s = 0.0f;
-    for (int w = 0; w < kDnWarps; ++w) s += accw[w * a.T * kRows + i];
-    const int tok = i / kRows, row = i % 16, tile = blockIdx.x * kDnTiles + (i % kRows) / 16;
-    const int col = 128 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
-    const __nv_bfloat16 b = __float2bfloat16_rn(s);
-    a.out[(int64_t)tok * a.ldo + col] = *reinterpret_cast<const uint16_t*>(&b);
+    __syncthreads();
+    const int64_t b0 = block_of((int64_t)grp * n), b1 = block_of((int64_t)grp * n + n - 1);
+    if (b0 == b1) {
+      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
+        float v = 0.0f;
+        for (int w = 0; w < kDnWarps; ++w) v += accw[w * elems + i];
+        store(grp, i, v);
+      }
+    } else {
+      // a block shares at most two groups of columns: the one that it enters in the middle (or
+      // before its end) and the one that it leaves unfinished
+      float* slot_out = a.partial + ((int64_t)blockIdx.x * 2 + (part > 0)) * elems;
+      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
+        float v = 0.0f;
+        for (int w = 0; w < kDnWarps; ++w) v += accw[w * elems + i];
+        __stcg(slot_out + i, v);
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) last = atomicAdd(arrived + grp, 1) == (int)(b1 - b0);
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
+          float v = 0.0f;
+          for (int64_t b = b0; b <= b1; ++b) {
+            // block b's part of this group: its first stretch, or its second where it began before
+            const bool second = bound(b) < (int64_t)grp * n;
+            v += __ldcg(a.partial + (b * 2 + second) * elems + i);
+          }
+          store(grp, i, v);
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
-size_t moe_few_list_words(int64_t T, int32_t k, int32_t E) {
-  const int64_t P = T * k;
-  return (size_t)(kListHead + 2 * ((P < E ? P : E) + 1) + P);
+size_t moe_few_list_words(int64_t T, int32_t k, int32_t E, int64_t H) {
+  const int P = (int)(T * k);
+  return (size_t)(kListHead + 3 * max_slots(P, E) + P + H / kDnRows);
 }
+
+constexpr int kDnMaxBlocks = 2 * 160;
+size_t moe_few_partial_floats(int64_t T) { return (size_t)kDnMaxBlocks * 2 * (size_t)T * kDnRows; }
 
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st) {
-  const int64_t P = (int64_t)a.T * a.k;
-  const int64_t items = (P < a.E ? P : a.E) * (a.I / 8 / kTiles);
-  const int64_t slots = 4 * (int64_t)num_sms;
-  moe_few_gate_up_kernel<<<(unsigned)(items < slots ? items : slots), kWarps * 32, 0, st>>>(a);
+  const int P = a.T * a.k;
+  const int64_t slots = max_slots(P, a.E);
+  const int64_t items = slots * (a.I / 8 / kTiles), room = 4 * (int64_t)num_sms;
+  moe_few_gate_up_kernel<<<(unsigned)(items < room ? items : room), kWarps * 32, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int smem = kDnWarps * a.T * 16 * kDnTiles * (int)sizeof(float);
+  const int smem = kDnWarps * a.T * kDnRows * (int)sizeof(float);
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(moe_few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  moe_few_down_kernel<<<(unsigned)(a.H / 16 / kDnTiles), kDnWarps * 32, smem, st>>>(a);
+  int64_t blocks = slots * (a.H / kDnRows);
+  if (blocks > 2 * (int64_t)num_sms) blocks = 2 * (int64_t)num_sms;
+  if (blocks > kDnMaxBlocks) blocks = kDnMaxBlocks;
+  moe_few_down_kernel<<<(unsigned)blocks, kDnWarps * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 
