@@ -502,7 +502,7 @@ nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const fl
 /*   ids         [T] int32 (id_bytes 4) or int64 (8).  id < 0 marks a padding row, which is not   */
 /*               read: logprob and entropy 0, top_ids -1, top_logprob 0, gradient 0.  id >= V is  */
 /*               NVFP4_ERR_INVALID_ARG in *dev_status and the row is treated as padding.          */
-/*   inv_temperature  1 / temperature, in (0, 1e30].                                             */
+/*   inv_temperature  1 / temperature, in [2^-26, 2^26].                                         */
 /*   logprob     float32 [T]; entropy optional float32 [T], in nats.                              */
 /*   stats       optional float32 [T x 4], 16-byte aligned: what the backward call needs.         */
 /*   k_top       alternatives per row, 0 .. min(32, V): top_ids int32 [T x k_top] by logit        */

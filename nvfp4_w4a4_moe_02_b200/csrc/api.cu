@@ -1245,8 +1245,8 @@ nvfp4_status check_logprobs(const void* logits, nvfp4_dtype dtype, int64_t T, in
   if (id_bytes != 4 && id_bytes != 8) return fail(NVFP4_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
   if (T < 0 || T > INT32_MAX || V <= 0 || V > INT32_MAX)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "0 <= T, 0 < V required, both at most INT32_MAX");
-  if (!(inv_temperature > 0.0f) || !(inv_temperature <= 1e30f))
-    return fail(NVFP4_ERR_INVALID_ARG, "inv_temperature must be positive and at most 1e30");
+  if (!(inv_temperature >= 1.4901161e-8f) || !(inv_temperature <= 67108864.0f))
+    return fail(NVFP4_ERR_INVALID_ARG, "inv_temperature must be in [2^-26, 2^26]");
   if (T == 0) return NVFP4_OK;
   if (!logits || !ids) return fail(NVFP4_ERR_INVALID_ARG, "logits / ids is NULL");
   const uintptr_t esz = dtype == NVFP4_OUT_F32 ? 4 : 2;
@@ -1291,7 +1291,7 @@ nvfp4_status token_logprobs_backward(const void* logits, nvfp4_dtype dtype, int6
     return fail(NVFP4_ERR_INVALID_ARG, "in place needs ldg == ldl");
   LogprobBwdArgs a{logits, T, V, ldl, dtype == NVFP4_OUT_BF16, ids, id_bytes, inv_temperature, stats, grad_logprob,
                    grad_entropy, grad_logits, ldg, dev_status};
-  cudaError_t e = launch_logprobs_backward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_logprobs_backward(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "log probability backward launch");
 }
 

@@ -263,7 +263,7 @@ struct LogprobArgs {
   int32_t k_top;
   float* logprob;              // [T]
   float* entropy;              // optional [T]
-  float* stats;                // optional [T x 4]: max logit, log2 of the sum, entropy
+  float* stats;                // optional [T x 4]: max logit, its reference M, log2 of the sum, entropy
   int32_t* top_ids;            // [T x k_top]
   float* top_lp;               // [T x k_top]
   int32_t* status;
@@ -282,7 +282,7 @@ struct LogprobBwdArgs {
   int64_t ldg;
   int32_t* status;
 };
-cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t st);
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int32_t* status, cudaStream_t st);
 

@@ -2,11 +2,17 @@
 // alternatives, and their gradient: the two sides of the rollout-trainer log-prob gap.
 //
 // With z = l / temperature over a row l of V logits, m = max l, c = log2(e) / temperature:
-//   y_v = (l_v - m) c,  s = sum 2^y_v,  u = sum 2^y_v y_v        (one pass, running maximum)
-//   logprob = (l_id - m) / temperature - ln s,  entropy = ln2 (log2 s - u / s)
-//   d l_v = ( g_lp (1[v = id] - p_v) - g_H p_v (ln p_v + H) ) / temperature,  p_v = 2^(y_v - log2 s)
-// The difference l - m is taken before the product with c: it is exact at the maximum, and a row
-// held at the type's lowest value stays finite.  All sums and statistics are binary32.
+//   y_v = l_v c - M with M = RN(m c),  s = sum 2^y_v,  u = sum 2^y_v y_v   (one pass, running maximum)
+//   logprob = ln2 (y_id - log2 s),  entropy = ln2 (log2 s - u / s)
+//   d l_v = ( g_lp (1[v = id] - p_v) - g_H p_v (ln p_v + H) ) / temperature,  p_v = 2^y_v / s
+// M is the reference itself, not an approximation of one: its rounding changes nothing, and y is
+// rounded once.  All sums and statistics are binary32.
+//
+// The forward pass reads the logits once and the backward pass reads and writes once, both bound by
+// memory; on the way there the exponentials (16 a clock and SM against 11.6 bf16 logits) and the
+// instructions come next, so sums and products go in pairs (fma.rn.f32x2) and masks cost one packed
+// maximum: logits below kLow count as kLow, 2^y = 0 then, and y stays finite.  A row whose largest
+// logit is not above kLow (masked by the type's lowest value, or all -inf) is done again exactly.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -16,6 +22,12 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
+// -2^100, a bf16: for c in [2^-26, 2^27] kLow c is finite, and 2^(kLow c - M) is 0 for every M above it
+constexpr float kLow = -1.2676506002282294e30f;
+constexpr uint32_t kLowBf16x2 = 0xF180F180u;
+// A row that the fast form cannot hold: nothing above kLow, or |M| so large that its rounding (y at the
+// maximum, up to 2^-25 |M|) would no longer be a small power of two
+__device__ __forceinline__ bool needs_exact(float m, float M) { return !(m > kLow && fabsf(M) < 268435456.0f); }
 
 __device__ __forceinline__ float ex2(float y) {
   float r;
@@ -34,7 +46,19 @@ struct Vec<float> {
     x[2] = __uint_as_float(r.z);
     x[3] = __uint_as_float(r.w);
   }
-  static __device__ __forceinline__ float get(const float* p) { return __ldg(p); }
+  // x_i = max(l_i, kLow), NaN kept; returns the largest l, NaN skipped
+  static __device__ __forceinline__ float clamp(uint4& r) {
+    uint32_t* w = &r.x;
+    const float m = fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(__uint_as_float(w[i])), "f"(kLow));
+      w[i] = __float_as_uint(v);
+    }
+    return m;
+  }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
   static __device__ __forceinline__ uint4 pack(const float* x) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
@@ -51,7 +75,19 @@ struct Vec<uint16_t> {  // bf16 bit patterns
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-  static __device__ __forceinline__ float get(const uint16_t* p) { return bf16_bits_to_f32(__ldg(p)); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t v;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(a), "r"(b));
+    return v;
+  }
+  static __device__ __forceinline__ float clamp(uint4& r) {
+    const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
+    uint32_t* w = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(kLowBf16x2));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ float get(const uint16_t* p) { return bf16_bits_to_f32(*p); }
   static __device__ __forceinline__ uint4 pack(const float* x) {
     uint32_t w[4];
 #pragma unroll
@@ -67,69 +103,103 @@ struct Vec<uint16_t> {  // bf16 bit patterns
   }
 };
 
-// Running statistics of a part of a row.  No element yet, or only -inf: m = -inf, s = u = 0.
-// A NaN or +inf among the elements ends as s = NaN.
-struct Stat {
-  float m, s, u;
+constexpr int64_t kWarpRow = 1024;  // rows up to this length go to a warp each
+
+// Running statistics of a part of a row against the reference M = RN(m c), m the largest logit seen.
+// Nothing above kLow yet: m is what it is, M = -inf, s = u = 0.  A NaN or +inf ends as s = NaN.
+struct __align__(16) Stat {
+  float m, M, s, u;
 };
 
-__device__ __forceinline__ Stat combine(const Stat& a, const Stat& b, float c) {
-  Stat r;
-  r.m = fmaxf(a.m, b.m);
-  r.s = 0.0f;
-  r.u = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const Stat& q = i ? b : a;
-    if (q.m == -INFINITY) {
-      r.s += q.s;  // 0, or NaN
-    } else {
-      const float d = (q.m - r.m) * c;
-      const float f = ex2(d);
-      r.s += f * q.s;
-      // a part 2^-150 below the maximum adds nothing; its d times s could be -inf times 0
-      if (f > 0.0f || !(d <= 0.0f)) r.u += f * (q.u + d * q.s);
-    }
-  }
-  return r;
+// Scales a part to the reference M (>= its own).
+__device__ __forceinline__ void rebase(Stat& a, float M) {
+  const float d = a.M - M;
+  const float f = ex2(d);
+  // a part 2^-126 below adds nothing, and one without elements has d = -inf; NaN stays NaN
+  a.u = f == 0.0f ? 0.0f * a.s : f * fmaf(d, a.s, a.u);
+  a.s *= f;
+  a.M = M;
 }
 
-// Adds n elements to a part: one rescale per call, when its maximum rises.
-template <int N>
-__device__ __forceinline__ void add_elements(Stat& a, const float* x, float c) {
-  float bm = x[0];
+// Joins the parts of n (a power of two) consecutive lanes; every lane gets the result, the same bits.
+template <int n>
+__device__ __forceinline__ void join_lanes(Stat& a) {
+  float m = a.m, M = a.M;
 #pragma unroll
-  for (int i = 1; i < N; ++i) bm = fmaxf(bm, x[i]);  // skips NaN
+  for (int o = n / 2; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  }
+  if (M > -INFINITY) rebase(a, M);  // else every s is 0 or NaN
+  a.m = m;
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
+  }
+}
+
+// Adds U x N logits to a part.
+template <typename L, int U>
+__device__ __forceinline__ void add_vectors(Stat& a, uint4 (&r)[U], float c) {
+  constexpr int N = Vec<L>::N;
+  float bm = Vec<L>::clamp(r[0]);
+#pragma unroll
+  for (int i = 1; i < U; ++i) bm = fmaxf(bm, Vec<L>::clamp(r[i]));
   if (!(bm <= a.m)) {
-    if (a.m > -INFINITY) {
-      const float d = (a.m - bm) * c;
-      const float f = ex2(d);
-      a.u = f > 0.0f ? f * (a.u + d * a.s) : 0.0f;
-      a.s *= f;
-    }
     a.m = fmaxf(a.m, bm);
+    if (a.m > kLow) rebase(a, a.m * c);
   }
-  if (a.m == -INFINITY) {
+  // while nothing is above kLow the elements are skipped: they add nothing to a row that has more, and
+  // the others are done again; a NaN must not be lost
+  const float M = a.M > -INFINITY ? a.M : 0.0f;
+  const float2 c2 = make_float2(c, c), M2 = make_float2(-M, -M);
+  float2 s = make_float2(0.0f, 0.0f), u = s;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (x[i] != x[i]) a.s = x[i];
-    return;
+  for (int i = 0; i < U; ++i) {
+    float x[N];
+    Vec<L>::unpack(r[i], x);
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), c2, M2);
+      const float2 e = make_float2(ex2(y.x), ex2(y.y));
+      s = __fadd2_rn(s, e);
+      u = __ffma2_rn(e, y, u);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = (x[i] - a.m) * c;
+  a.s += s.x + s.y;
+  a.u += u.x + u.y;
+}
+
+// A row's edges go element by element.
+__device__ __forceinline__ void add_element(Stat& a, float x, float c) {
+  if (x != x) a.s = x;
+  if (x > a.m) {
+    a.m = x;
+    if (x > kLow) rebase(a, x * c);
+  }
+  if (a.M > -INFINITY) {
+    const float y = fmaf(fmaxf(x, kLow), c, -a.M);
     const float e = ex2(y);
     a.s += e;
-    a.u = fmaf(e, fmaxf(y, -1000.0f), a.u);  // -inf: e = 0 times a finite number
+    a.u = fmaf(e, y, a.u);
   }
-  // fmaxf drops a NaN, but s keeps it
+}
+// The exact form: m is the row's largest logit.
+__device__ __forceinline__ void add_exact(float& s, float& u, float x, float m, float c) {
+  const float y = (x - m) * c;
+  const float e = ex2(y);
+  s += e;
+  u = fmaf(e, fmaxf(y, -1000.0f), u);
 }
 
 // Order of the alternatives: value descending, index ascending, as one unsigned key (0 = none).
-__device__ __forceinline__ uint64_t order_key(float v, uint32_t idx) {
+__device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);  // -0 ties with +0
-  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((uint64_t)k << 32) | (0xFFFFFFFFu - idx);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(float v, uint32_t idx) {
+  return ((uint64_t)order_bits(v) << 32) | (0xFFFFFFFFu - idx);
 }
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t k = (uint32_t)(key >> 32);
@@ -137,48 +207,51 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 }
 __device__ __forceinline__ int32_t key_index(uint64_t key) { return (int32_t)(0xFFFFFFFFu - (uint32_t)key); }
 
-// A warp's best 32 keys, lane i holding the i-th; thr is the k-th.
+// A warp's best 32 keys, lane i holding the i-th; thr: a key is taken if it is above.
 __device__ __forceinline__ void insert_key(uint64_t& mine, uint64_t& thr, uint64_t key, int k) {
   const int lane = threadIdx.x & 31;
   const int pos = __popc(__ballot_sync(0xffffffffu, mine > key));
   const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
   if (lane == pos) mine = key;
   if (lane > pos) mine = up;
-  thr = __shfl_sync(0xffffffffu, mine, k - 1);
+  const uint64_t kth = __shfl_sync(0xffffffffu, mine, k - 1);
+  thr = kth > thr ? kth : thr;
 }
 
-template <int N>
-__device__ __forceinline__ void offer(uint64_t& mine, uint64_t& thr, const float* x, uint32_t idx0, int n, int k) {
-  // one key per lane first: its largest element stands for the others
-  uint64_t best = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint64_t q = i < n ? order_key(x[i], idx0 + i) : 0;
-    best = q > best ? q : best;
-  }
-  uint32_t mask = __ballot_sync(0xffffffffu, best > thr);
+// One logit per lane (`has` false: none).
+__device__ __forceinline__ void offer(uint64_t& mine, uint64_t& thr, float x, uint32_t idx, bool has, int k) {
+  const uint64_t key = has ? order_key(x, idx) : 0;
+  uint32_t mask = __ballot_sync(0xffffffffu, key > thr);
   while (mask) {
-    const int src = __ffs(mask) - 1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint64_t q = __shfl_sync(0xffffffffu, i < n ? order_key(x[i], idx0 + i) : 0ull, src);
-      if (q > thr) insert_key(mine, thr, q, k);
-    }
-    mask &= __ballot_sync(0xffffffffu, best > thr) & ~((2u << src) - 1u);
+    const uint64_t q = __shfl_sync(0xffffffffu, key, __ffs(mask) - 1);
+    if (q > thr) insert_key(mine, thr, q, k);
+    mask &= mask - 1;
   }
 }
 
+// Sorts one value per lane, descending.
+__device__ __forceinline__ float sort_lanes(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+      v = keep_max ? fmaxf(v, w) : fminf(v, w);
+    }
+  }
+  return v;
+}
 // Two descending lists -> their best 32, descending: the element-wise maximum of one and the other
 // reversed is bitonic and holds them; five exchanges sort it.
-__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b) {
+__device__ __forceinline__ float merge_lanes(float a, float b) {
   const int lane = threadIdx.x & 31;
-  const uint64_t r = __shfl_xor_sync(0xffffffffu, b, 31);
-  uint64_t v = a > r ? a : r;
+  float v = fmaxf(a, __shfl_xor_sync(0xffffffffu, b, 31));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    const bool keep_max = (lane & o) == 0;
-    v = keep_max == (v > w) ? v : w;
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = (lane & o) == 0 ? fmaxf(v, w) : fminf(v, w);
   }
   return v;
 }
@@ -188,33 +261,86 @@ __device__ __forceinline__ int64_t read_id(const void* ids, int id_bytes, int64_
                        : (int64_t)__ldg(reinterpret_cast<const int*>(ids) + t);
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Stores to the same variable of the cluster's first block.
+__device__ __forceinline__ uint32_t first_block(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)));
+  return r;
+}
+__device__ __forceinline__ void store_remote(Stat* p, const Stat& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+               :
+               : "r"(first_block(p)), "f"(v.m), "f"(v.M), "f"(v.s), "f"(v.u)
+               : "memory");
+}
+__device__ __forceinline__ void store_remote(uint64_t* p, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" : : "r"(first_block(p)), "l"(v) : "memory");
+}
+
+// A row, or a block's share of one: elements before the first 16-byte boundary and after the last one
+// go one by one (at most 14, all to the share that has any).
+template <typename L>
+struct Span {
+  const L* row;
+  int64_t lo, hi;    // this share's vectors
+  int64_t head, V;
+  int edge;          // elements that go one by one here
+  __device__ __forceinline__ Span(const L* r, int64_t v, int part, int parts) : row(r), V(v) {
+    constexpr int N = Vec<L>::N;
+    head = min(v, (int64_t)((16 - (reinterpret_cast<uintptr_t>(r) & 15)) & 15) / (int64_t)sizeof(L));
+    const int64_t nvec = (v - head) / N;
+    lo = nvec * part / parts;
+    hi = nvec * (part + 1) / parts;
+    edge = part == 0 ? (int)(v - nvec * N) : 0;
+  }
+  __device__ __forceinline__ int64_t edge_index(int i) const { return i < head ? i : V - edge + i; }
+  __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(row + head); }
+};
+
 }  // namespace
 
-// One row per team of W warps; a block holds one team (W > 1) or eight one-warp teams.
+// One row per team.  W > 1: a team is a cluster of `parts` blocks of W warps, each with its share of
+// the row, joined through the cluster's shared memory; W = 1: a block holds eight one-warp teams.
+//
+// Alternatives: every thread knows the largest of its logits; the k-th largest of these, tau, is a
+// lower bound of the k-th alternative, and only threads whose largest is not below it can hold one.
+// Their logits (k threads' worth unless logits tie) are read again and sorted in; a block's best k
+// then take their places by counting the larger ones.
 template <typename L, int W, bool TOP>
-__global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobArgs a) {
+__global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobArgs a, int parts) {
   constexpr int N = Vec<L>::N;
   constexpr int kTeam = W * 32;
-  __shared__ Stat part[W];
-  __shared__ uint64_t lists[TOP ? W : 1][32];
+  constexpr int U = 4;
+  constexpr int kMaxParts = 8;
+  __shared__ Stat part_stat[W > 1 ? W : 1];
+  __shared__ float maxima[TOP && W > 1 ? W : 1][32];
+  __shared__ uint64_t cand[TOP && W > 1 ? W : 1][32];
+  __shared__ uint64_t best[32];
+  // of the cluster's blocks, in the first one
+  __shared__ Stat team_stat[kMaxParts];
+  __shared__ uint64_t team_best[TOP && W > 1 ? kMaxParts * 32 : 1];
   const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int tid = W > 1 ? threadIdx.x : lane;
-  const int warp = W > 1 ? threadIdx.x >> 5 : 0;
-  const int64_t t = W > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int part = W > 1 ? (int)(blockIdx.x % parts) : 0;
+  const int64_t t = W > 1 ? (int64_t)(blockIdx.x / parts) : (int64_t)blockIdx.x * 8 + warp;
   if (t >= a.T) return;
   const int k = a.k_top;
   int64_t id = read_id(a.ids, a.id_bytes, t);
+  const bool first = part == 0 && tid == 0;
   if (id >= a.V) {
-    if (tid == 0) report_status(a.status, kErrInvalid);
+    if (first) report_status(a.status, kErrInvalid);
     id = -1;
   }
-  if (id < 0) {  // padding: the row is not read
-    if (tid == 0) {
+  if (id < 0) {  // padding: the row is not read (all of a cluster leave here)
+    if (first) {
       a.logprob[t] = 0.0f;
       if (a.entropy) a.entropy[t] = 0.0f;
       if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    if (TOP && tid < k) {
+    if (TOP && part == 0 && tid < k) {
       a.top_ids[t * k + tid] = -1;
       a.top_lp[t * k + tid] = 0.0f;
     }
@@ -222,144 +348,328 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
   }
   const float c = a.inv_temp * kLog2e;
   const L* row = reinterpret_cast<const L*>(a.logits) + t * a.ld;
-  const int64_t V = a.V;
-
-  Stat st{-INFINITY, 0.0f, 0.0f};
-  uint64_t mine = 0, thr = 0;
-  // the elements before the first 16-byte boundary and those after the last one go one by one
-  const int64_t head = min(V, (int64_t)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int64_t)sizeof(L));
-  const int64_t nvec = (V - head) / N;
-  const int64_t tail0 = head + nvec * N;
-  const int edge = (int)(head + (V - tail0));
-  {
-    float x = -INFINITY;
-    const int64_t v = lane < head ? lane : tail0 + (lane - head);
-    const bool has = warp == 0 && lane < edge;
-    if (has) {
-      x = Vec<L>::get(row + v);
-      add_elements<1>(st, &x, c);
-    }
-    if (TOP && warp == 0) offer<1>(mine, thr, &x, (uint32_t)v, has ? 1 : 0, k);
+  const Span<L> sp(row, a.V, part, parts);
+  if (W > 1 && parts > 1) {
+    __syncwarp();
+    cluster_arrive();
   }
-  const uint4* vrow = reinterpret_cast<const uint4*>(row + head);
-  constexpr int U = 4;
-  for (int64_t v0 = 0; v0 < nvec; v0 += kTeam * U) {
+  float l_id = 0.0f;
+  if (first) l_id = Vec<L>::get(row + id);
+
+  Stat st{-INFINITY, -INFINITY, 0.0f, 0.0f};
+  int64_t v = sp.lo + tid;
+  for (; v + (U - 1) * kTeam < sp.hi; v += U * kTeam) {
     uint4 r[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t v = v0 + i * kTeam + tid;
-      if (v < nvec) r[i] = __ldg(vrow + v);
-    }
+    for (int i = 0; i < U; ++i) r[i] = __ldg(sp.vec() + v + i * kTeam);
+    add_vectors<L, U>(st, r, c);
+  }
+  {
+    uint4 r[U - 1];
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t v = v0 + i * kTeam + tid;
-      const bool has = v < nvec;
-      float x[N];
-      if (has) {
-        Vec<L>::unpack(r[i], x);
-        add_elements<N>(st, x, c);
+    for (int i = 0; i < U - 1; ++i) {
+      // absent vectors: -inf, which adds nothing
+      r[i] = sizeof(L) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                            : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+      if (v + i * kTeam < sp.hi) {
+        r[i] = __ldg(sp.vec() + v + i * kTeam);
+        any = true;
       }
-      if (TOP) offer<N>(mine, thr, x, (uint32_t)(head + v * N), has ? N : 0, k);
+    }
+    if (any) add_vectors<L, U - 1>(st, r, c);
+  }
+  if (tid < sp.edge) add_element(st, Vec<L>::get(row + sp.edge_index(tid)), c);
+  // the largest logit of this thread: where it is not above kLow, the maximum was taken all the same
+  const float own_max = st.m;
+
+  join_lanes<32>(st);
+  float tau = -INFINITY;
+  uint64_t mine = 0, thr = 0;
+  if (W > 1) {
+    float sorted = 0.0f;
+    if (lane == 0) part_stat[warp] = st;
+    if (TOP) {
+      sorted = sort_lanes(own_max);
+      maxima[warp][lane] = sorted;
+    }
+    __syncthreads();
+    st = part_stat[lane & (W - 1)];
+    join_lanes<W>(st);
+    if (TOP) {
+#pragma unroll
+      for (int o = 1; o < W; o <<= 1) {  // lists of 2 o warps meet in the first of them
+        if ((warp & (2 * o - 1)) == 0) {
+          sorted = merge_lanes(sorted, maxima[warp + o][lane]);
+          maxima[warp][lane] = sorted;
+        }
+        __syncthreads();
+      }
+      tau = maxima[0][k - 1];
+    }
+  } else if (TOP) {
+    tau = __shfl_sync(0xffffffffu, sort_lanes(own_max), k - 1);
+  }
+  if (TOP) {
+    thr = (uint64_t)order_bits(tau) << 32;  // below every logit that is not below tau
+    uint32_t holders = __ballot_sync(0xffffffffu, !(own_max < tau));
+    while (holders) {
+      const int src = __ffs(holders) - 1;
+      holders &= holders - 1;
+      const int64_t v0 = sp.lo + (W > 1 ? warp * 32 : 0) + src;
+      for (int64_t b = v0; b < sp.hi; b += 32 * kTeam) {  // a vector of that thread per lane
+        const int64_t w = b + (int64_t)lane * kTeam;
+        float x[N];
+        const bool has = w < sp.hi;
+        if (has) {
+          const uint4 r = __ldg(sp.vec() + w);
+          Vec<L>::unpack(r, x);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) offer(mine, thr, has ? x[i] : 0.0f, (uint32_t)(sp.head + w * N + i), has, k);
+      }
+    }
+    if (W == 1 || warp == 0) {
+      const bool has = lane < sp.edge;
+      const int64_t i = has ? sp.edge_index(lane) : 0;
+      offer(mine, thr, has ? Vec<L>::get(row + i) : 0.0f, (uint32_t)i, has, k);
     }
   }
-  // join the lanes, then the warps
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat q;
-    q.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    q.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    q.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-    // the same order of the two in both lanes: the sums come out equal
-    st = (lane & o) ? combine(q, st, c) : combine(st, q, c);
-  }
-  if (W > 1) {
-    if (lane == 0) part[warp] = st;
-    if (TOP) lists[warp][lane] = mine;
+
+  if (TOP && W > 1) {
+    // a key's place is the number of larger ones; the block's best k, in order
+    cand[warp][lane] = lane < k ? mine : 0;
+    if (warp == 0) best[lane] = 0;
     __syncthreads();
-    if (warp != 0) return;
-    st = part[0];
-    for (int w = 1; w < W; ++w) st = combine(st, part[w], c);
-    if (TOP)
-      for (int w = 1; w < W; ++w) mine = merge_lists(mine, lists[w][lane]);
+    const uint64_t key = cand[warp][lane];
+    if (key != 0) {
+      int place = 0;
+      for (int i = 0; i < W; ++i)
+        for (int j = 0; j < k && cand[i][j] > key; ++j) ++place;
+      if (place < k) best[place] = key;
+    }
+    __syncthreads();
   }
-  const bool empty = st.m == -INFINITY && st.s == 0.0f;  // every logit is -inf: no distribution
+  uint64_t key = 0;
+  int place = 32;
+  if (W > 1 && parts > 1) {
+    cluster_wait();  // every block of the cluster runs: the first one's shared memory may be written
+    if (tid == 0) store_remote(&team_stat[part], st);
+    if (TOP && tid < 32) store_remote(&team_best[32 * part + tid], best[tid]);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (part != 0) return;
+    st = Stat{-INFINITY, -INFINITY, 0.0f, 0.0f};
+    if ((lane & (kMaxParts - 1)) < parts) st = team_stat[lane & (kMaxParts - 1)];
+    join_lanes<kMaxParts>(st);
+    if (TOP && tid < 32 * parts) {
+      key = team_best[tid];
+      if (key != 0) {
+        place = 0;
+        for (int i = 0; i < parts; ++i)
+          for (int j = 0; j < k && team_best[32 * i + j] > key; ++j) ++place;
+      }
+    }
+  } else if (TOP && tid < 32) {
+    key = W > 1 ? best[tid] : mine;
+    place = tid;
+  }
+
+  // m = -inf and no NaN: no distribution
+  const bool empty = st.m == -INFINITY && st.s == 0.0f;
+  if (st.m > -INFINITY && needs_exact(st.m, st.M)) {
+    float s = 0.0f, u = 0.0f;
+    for (int64_t i = tid; i < a.V; i += kTeam) add_exact(s, u, Vec<L>::get(row + i), st.m, c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      u += __shfl_xor_sync(0xffffffffu, u, o);
+    }
+    if (W > 1) {
+      __syncthreads();
+      if (lane == 0) part_stat[warp] = Stat{0.0f, 0.0f, s, u};
+      __syncthreads();
+      s = u = 0.0f;
+      for (int w = 0; w < W; ++w) {
+        s += part_stat[w].s;
+        u += part_stat[w].u;
+      }
+    }
+    st.s = s;
+    st.u = u;
+  }
   const float ls = empty ? 0.0f : log2f(st.s);
-  if (lane == 0) {
-    if (!empty && !(st.s < INFINITY)) report_status(a.status, kErrRange);
-    // in nats from here: a finite log prob near the type's lowest value does not overflow on the way
-    const float y = (Vec<L>::get(row + id) - st.m) * a.inv_temp;
-    const float h = empty ? 0.0f : fmaxf((ls - st.u / st.s) * kLn2, 0.0f) + (st.s - st.s);
-    a.logprob[t] = empty ? -INFINITY : fmaf(ls, -kLn2, y);
+  const bool exact = needs_exact(st.m, st.M);
+  auto log_prob = [&](float l) {
+    // in nats where the pairs' form could overflow on the way to a finite result
+    if (empty) return -INFINITY;
+    if (exact || !(l > kLow)) return fmaf(ls, -kLn2, (l - st.m) * a.inv_temp);
+    return (fmaf(l, c, -st.M) - ls) * kLn2;
+  };
+  if (tid == 0) {
+    const bool bad = !empty && !(st.s < INFINITY);
+    if (bad) report_status(a.status, kErrRange);
+    const float h = empty ? 0.0f : bad ? NAN : fmaxf((ls - st.u / st.s) * kLn2, 0.0f);
+    a.logprob[t] = bad ? NAN : log_prob(l_id);
     if (a.entropy) a.entropy[t] = h;
-    // m = -inf marks the row without a distribution: its gradient is zero
-    const float m = !empty && st.m == -INFINITY ? st.s : st.m;
-    if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(m, ls, h, 0.0f);
+    if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(bad ? NAN : st.m, st.M, ls, h);
   }
-  if (TOP && lane < k) {
-    a.top_ids[t * k + lane] = key_index(mine);
-    a.top_lp[t * k + lane] = empty ? -INFINITY : fmaf(ls, -kLn2, (key_value(mine) - st.m) * a.inv_temp);
+  if (TOP && place < k && (key != 0 || place == tid)) {
+    a.top_ids[t * k + place] = key_index(key);
+    a.top_lp[t * k + place] = !empty && !(st.s < INFINITY) ? NAN : log_prob(key_value(key));
   }
 }
 
-// dlogits of one stretch of a row; 16-byte loads where the row allows, 16-byte stores where the
-// gradient's row has the same phase.
-template <typename L>
-__global__ void __launch_bounds__(256) logprobs_backward_kernel(LogprobBwdArgs a) {
+// dlogits = 2^y (A + B y) + [v = id] g_lp / temperature, with the row's factors A, B.  W > 1: a block
+// takes a stretch of a row, W = 1: a warp takes a row.  16-byte accesses where the row of the logits and
+// of the gradient have the same phase.
+template <typename L, int W>
+__global__ void __launch_bounds__(256) logprobs_backward_kernel(LogprobBwdArgs a, int64_t stretches) {
   constexpr int N = Vec<L>::N;
-  const int64_t t = blockIdx.x;
+  constexpr int kTeam = W * 32;
+  constexpr int U = 4;
+  const int tid = W > 1 ? threadIdx.x : threadIdx.x & 31;
+  const int64_t unit = W > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t t = W > 1 ? unit / stretches : unit;
+  const int64_t at = W > 1 ? unit % stretches : 0;
+  if (t >= a.T) return;
   const L* row = reinterpret_cast<const L*>(a.logits) + t * a.ld;
   L* grow = reinterpret_cast<L*>(a.grad) + t * a.ldg;
   int64_t id = read_id(a.ids, a.id_bytes, t);
+  const float4 st = __ldg(reinterpret_cast<const float4*>(a.stats) + t);  // m, M, log2 s, entropy
   if (id >= a.V) {
-    if (threadIdx.x == 0) report_status(a.status, kErrInvalid);
+    if (tid == 0 && at == 0) report_status(a.status, kErrInvalid);
     id = -1;
   }
-  const float4 stt = __ldg(reinterpret_cast<const float4*>(a.stats) + t);
   const float c = a.inv_temp * kLog2e;
+  const bool zero = id < 0 || st.x == -INFINITY;
+  const bool exact = needs_exact(st.x, st.y);
   float ga = 0.0f, gb = 0.0f;
-  const bool zero = id < 0 || stt.x == -INFINITY;
   if (!zero) {
     if (a.g_lp) ga = __ldg(a.g_lp + t) * a.inv_temp;
     if (a.g_ent) gb = __ldg(a.g_ent + t) * a.inv_temp;
   }
-  auto grad = [&](float l, int64_t v) {
-    const float q = fmaxf((l - stt.x) * c - stt.y, -1000.0f);  // log2 p; p = 0 below
-    const float p = ex2(q);
-    const float w = fmaf(gb, fmaf(q, kLn2, stt.z), ga);
-    return (v == id ? ga : 0.0f) - p * w;
+  const float rs = ex2(-st.z);
+  const float A = -rs * fmaf(gb, fmaf(st.z, -kLn2, st.w), ga), B = -rs * gb * kLn2;
+  auto element = [&](float l, int64_t v) {
+    if (zero) return 0.0f;
+    float g;
+    if (exact) {
+      const float q = fmaxf((l - st.x) * c - st.z, -1000.0f);  // log2 p
+      g = -ex2(q) * fmaf(gb, fmaf(q, kLn2, st.w), ga) + (st.x - st.x);
+    } else {
+      const float y = fmaf(l > kLow ? l : l != l ? l : kLow, c, -st.y);
+      g = ex2(y) * fmaf(B, y, A);
+    }
+    return v == id ? g + ga : g;
   };
-  for (int64_t v = threadIdx.x; v < a.V; v += 256)
-    Vec<L>::put(grow + v, zero ? 0.0f : grad(Vec<L>::get(row + v), v));
-  (void)N;
+  const Span<L> sp(row, a.V, 0, 1);
+  if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grow)) & 15) != 0) {
+    const int64_t per = (a.V + stretches - 1) / stretches;
+    const int64_t end = min(a.V, (at + 1) * per);
+    for (int64_t v = at * per + tid; v < end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
+    return;
+  }
+  uint4* gvec = reinterpret_cast<uint4*>(grow + sp.head);
+  const int64_t lo = sp.hi * at / stretches, hi = sp.hi * (at + 1) / stretches;
+  const float2 c2 = make_float2(c, c), M2 = make_float2(-st.y, -st.y);
+  const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
+  for (int64_t v0 = lo + tid; v0 < hi; v0 += U * kTeam) {
+    uint4 r[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) r[i] = v0 + i * kTeam < hi && !zero ? sp.vec()[v0 + i * kTeam] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t v = v0 + i * kTeam;
+      if (v >= hi) break;
+      const int64_t e0 = sp.head + v * N;
+      float x[N];
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = 0.0f;
+      } else if (exact) {
+        Vec<L>::unpack(r[i], x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = element(x[j], e0 + j);
+      } else {
+        Vec<L>::clamp(r[i]);
+        Vec<L>::unpack(r[i], x);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), c2, M2);
+          const float2 g = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), __ffma2_rn(B2, y, A2));
+          x[j] = g.x;
+          x[j + 1] = g.y;
+        }
+        if (id >= e0 && id < e0 + N) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (e0 + j == id) x[j] += ga;
+        }
+      }
+      gvec[v] = Vec<L>::pack(x);
+    }
+  }
+  if (at == 0 && tid < sp.edge) {
+    const int64_t v = sp.edge_index(tid);
+    Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
+  }
 }
+
+namespace {
+
+// Blocks per row: one, or as many as it takes to give every SM two blocks, while a block keeps 4096
+// logits to itself.
+int row_parts(int64_t T, int64_t V, int num_sms) {
+  int parts = 1;
+  while (parts < 8 && T * parts < 2 * (int64_t)num_sms && V >= 8192 * (int64_t)parts) parts *= 2;
+  return parts;
+}
+
+template <typename L, bool TOP>
+cudaError_t launch_forward(const LogprobArgs& a, int num_sms, cudaStream_t st) {
+  if (a.V <= kWarpRow) {
+    logprobs_kernel<L, 1, TOP><<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>(a, 1);
+    return cudaGetLastError();
+  }
+  const int parts = row_parts(a.T, a.V, num_sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.T * parts));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)parts;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<L, 8, TOP>, a, parts);
+}
+
+template <typename L>
+cudaError_t launch_backward(const LogprobBwdArgs& a, cudaStream_t st) {
+  if (a.V <= kWarpRow) {
+    logprobs_backward_kernel<L, 1><<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>(a, 1);
+    return cudaGetLastError();
+  }
+  // four vectors a thread, more where the grid would pass its limit
+  int64_t stretches = (a.V + 1024 * Vec<L>::N - 1) / (1024 * Vec<L>::N);
+  if (stretches > INT32_MAX / a.T) stretches = INT32_MAX / a.T;
+  logprobs_backward_kernel<L, 8><<<(unsigned)(a.T * stretches), 256, 0, st>>>(a, stretches);
+  return cudaGetLastError();
+}
+
+}  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-#define NVFP4_LP(L, W, TOP) logprobs_kernel<L, W, TOP><<<(unsigned)(W > 1 ? a.T : (a.T + 7) / 8), W > 1 ? W * 32 : 256, 0, st>>>(a)
-#define NVFP4_LP_W(L)                                                     \
-  do {                                                                    \
-    if (a.V <= 1024) {                                                    \
-      if (a.k_top > 0) NVFP4_LP(L, 1, true); else NVFP4_LP(L, 1, false);  \
-    } else {                                                              \
-      if (a.k_top > 0) NVFP4_LP(L, 8, true); else NVFP4_LP(L, 8, false);  \
-    }                                                                     \
-  } while (0)
   if (a.bf16)
-    NVFP4_LP_W(uint16_t);
-  else
-    NVFP4_LP_W(float);
-#undef NVFP4_LP_W
-#undef NVFP4_LP
-  return cudaGetLastError();
+    return a.k_top > 0 ? launch_forward<uint16_t, true>(a, num_sms, st) : launch_forward<uint16_t, false>(a, num_sms, st);
+  return a.k_top > 0 ? launch_forward<float, true>(a, num_sms, st) : launch_forward<float, false>(a, num_sms, st);
 }
 
-cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  if (a.bf16)
-    logprobs_backward_kernel<uint16_t><<<(unsigned)a.T, 256, 0, st>>>(a);
-  else
-    logprobs_backward_kernel<float><<<(unsigned)a.T, 256, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t st) {
+  return a.bf16 ? launch_backward<uint16_t>(a, st) : launch_backward<float>(a, st);
 }
 
 }  // namespace nvfp4
