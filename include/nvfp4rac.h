@@ -466,7 +466,7 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
                                           void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
-/* moe_w4a16_layer -- a whole MoE layer for a few tokens (T <= 64) in two kernels: routing,    */
+/* moe_w4a16_layer -- a whole MoE layer for a few tokens (T <= 64) in three kernels: routing,  */
 /* gate_up with SwiGLU, down and the weighted combine.  Activations stay bf16: at a few tokens */
 /* the layer is bound by the bytes of the touched experts' weights, so that nothing is gained  */
 /* by quantising them, no residual is needed (W_sel is not read), and the function is the      */
@@ -487,7 +487,7 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
 /*               the call.  dev_status may be NULL.                                              */
 /* An infinity or NaN in x reaches the outputs of its token by the usual arithmetic.            */
 /* ---------------------------------------------------------------------------------------- */
-size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int64_t H, int64_t I);
 nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
                              const nvfp4_tensor* w_gate_up, const nvfp4_tensor* w_down, int32_t* topk_ids,
                              float* topk_w, uint16_t* out, int64_t ldo, void* workspace, size_t workspace_bytes,

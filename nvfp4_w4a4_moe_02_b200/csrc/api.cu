@@ -1169,13 +1169,26 @@ nvfp4_status moe_combine(const uint16_t* y, int64_t ldy, int64_t y_rows, const i
 
 // ------------------------------------------------------------------------------------------ few-token layer
 namespace {
-size_t few_h_bytes(int64_t T, int32_t k, int64_t I) { return round_up((size_t)(T * k) * (size_t)I * sizeof(float), 256); }
-size_t few_partial_bytes(int64_t T) { return round_up(moe_few_partial_floats(T) * sizeof(float), 256); }
+// the parts of the layer's workspace, each on a 256-byte boundary
+enum { kFewXh, kFewXScale, kFewH, kFewHScale, kFewY, kFewLists, kFewParts };
+size_t few_workspace(int64_t T, int32_t k, int64_t H, int64_t I, size_t (&at)[kFewParts]) {
+  const size_t P = (size_t)(T * k);
+  const size_t bytes[kFewParts] = {(size_t)(T * H) * 2, (size_t)(T * (H / 128)) * 4, P * (size_t)I * 2,
+                                   P * (size_t)(I / 32) * 4, P * (size_t)H * 4,
+                                   moe_few_list_words(T, k, H) * sizeof(int32_t)};
+  size_t total = 0;
+  for (int i = 0; i < kFewParts; ++i) {
+    at[i] = total;
+    total += round_up(bytes[i], 256);
+  }
+  return total;
+}
 }  // namespace
 
-size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I) {
-  if (T <= 0 || T > kFewMaxTokens || k <= 0 || k > 32 || E <= 0 || H <= 0 || I <= 0) return 0;
-  return few_h_bytes(T, k, I) + few_partial_bytes(T) + round_up(moe_few_list_words(T, k, E, H) * sizeof(int32_t), 256);
+size_t moe_w4a16_workspace_size(int64_t T, int32_t k, int64_t H, int64_t I) {
+  if (T <= 0 || T > kFewMaxTokens || k <= 0 || k > 32 || H <= 0 || I <= 0) return 0;
+  size_t at[kFewParts];
+  return few_workspace(T, k, H, I, at);
 }
 
 nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int32_t k,
@@ -1206,7 +1219,7 @@ nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const fl
     return fail(NVFP4_ERR_ALIGNMENT, "x must be 16-byte aligned with a pitch >= H, a multiple of 8");
   if (ldo < H || ldo % 8 != 0 || !aligned16(out))
     return fail(NVFP4_ERR_ALIGNMENT, "out must be 16-byte aligned with a pitch >= H, a multiple of 8");
-  if (!workspace || workspace_bytes < moe_w4a16_workspace_size(T, k, (int32_t)E, H, I))
+  if (!workspace || workspace_bytes < moe_w4a16_workspace_size(T, k, H, I))
     return fail(NVFP4_ERR_INVALID_ARG, "workspace too small");
   if (!aligned16(workspace)) return fail(NVFP4_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   MoeFewArgs a;
@@ -1229,9 +1242,14 @@ nvfp4_status moe_w4a16_layer(const uint16_t* x, int64_t T, int64_t ldx, const fl
   a.out = out;
   a.ldo = ldo;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
-  a.h = reinterpret_cast<float*>(ws);
-  a.partial = reinterpret_cast<float*>(ws + few_h_bytes(T, k, I));
-  a.lists = reinterpret_cast<int32_t*>(ws + few_h_bytes(T, k, I) + few_partial_bytes(T));
+  size_t at[kFewParts];
+  few_workspace(T, k, H, I, at);
+  a.xh = reinterpret_cast<uint16_t*>(ws + at[kFewXh]);
+  a.x_scale = reinterpret_cast<float*>(ws + at[kFewXScale]);
+  a.h = reinterpret_cast<uint16_t*>(ws + at[kFewH]);
+  a.h_scale = reinterpret_cast<float*>(ws + at[kFewHScale]);
+  a.y = reinterpret_cast<float*>(ws + at[kFewY]);
+  a.lists = reinterpret_cast<int32_t*>(ws + at[kFewLists]);
   a.status = dev_status;
   cudaError_t e = launch_moe_few(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "few-token layer launch");

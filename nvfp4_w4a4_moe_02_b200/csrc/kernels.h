@@ -243,13 +243,16 @@ struct MoeFewArgs {
   float* topk_w;               // [T x k]
   uint16_t* out;               // bf16 [T x H], pitch ldo
   int64_t ldo;
-  float* h;                    // workspace: [T k x I] SwiGLU outputs, rows in expert order
-  float* partial;              // workspace: moe_few_partial_floats(T)
-  int32_t* lists;              // workspace: moe_few_list_words(T, k, E, H) words
+  // workspaces
+  uint16_t* xh;                // f16 [T x H]: scaled x
+  float* x_scale;              // [T x H / 128]: the powers of two taken out of x
+  uint16_t* h;                 // f16 [T k x I]: scaled SwiGLU outputs, rows in slot order
+  float* h_scale;              // [T k x I / 32]
+  float* y;                    // [T k x H]: outputs of the pairs, rows in slot order
+  int32_t* lists;              // moe_few_list_words(T, k, H) words
   int32_t* status;
 };
-size_t moe_few_list_words(int64_t T, int32_t k, int32_t E, int64_t H);
-size_t moe_few_partial_floats(int64_t T);
+size_t moe_few_list_words(int64_t T, int32_t k, int64_t H);
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st);
 
 // ---- token log probabilities (csrc/logprobs.cu)

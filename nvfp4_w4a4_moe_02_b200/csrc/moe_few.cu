@@ -1,22 +1,27 @@
-// A whole mixture-of-experts layer for a few tokens in two kernels: routing and gate_up with
-// SwiGLU, then down with the weighted combine.  Activations stay bf16 (the trainer's side of the
-// method: weights fake-quantised, activations not), weights are the packed NVFP4 ones.
+// A whole mixture-of-experts layer for a few tokens: a small kernel that routes and lays the work out,
+// gate_up with SwiGLU, and down with the weighted combine.  Activations stay bf16 (the trainer's side of
+// the method: weights fake-quantised, activations not), weights are the packed NVFP4 ones.
 //
 //   ids_t, w_t = the k largest logits of token t and their renormalised softmax
 //   h_tj = silu(G_e x_t) * (U_e x_t),  out_t = sum_j w_tj D_e h_tj,   e = ids_tj
 //
-// The weights of the experts that are touched bound it: each 16 x 128 tile of codes goes from
-// memory straight into registers and is decoded there into the A operand of mma.m16n8k16 (f16,
-// binary32 sums), the expert's tokens are its eight columns.
+// The weights of the experts that are touched bound it.  Up to eight tokens of one expert make a slot;
+// a unit of work is a slot times four 16-row tiles of the expert's matrix, streamed by one warp (or by
+// S warps that split K, where there are few units) through a ring in shared memory and decoded into the
+// A operand of mma.m16n8k16 (f16, binary32 sums); the slot's tokens are the eight columns.
 //   - E2M1 x E4M3 has at most six significant bits and lies in [2^-10, 2688]: exact in f16.
 //   - The sum over k may take its elements in any order, so a lane keeps the 32 consecutive codes
 //     of its 16-byte load: instruction i of a chunk contracts elements 4i .. 4i+3 of every lane.
-//   - Activations are scaled per token and 128-element chunk by a power of two that brings the
-//     chunk's largest to [2^14, 2^15), which keeps every bf16 down to 2^-31 of it exact in f16;
-//     the power is taken out of the chunk's sum.
-//   - A tile's 16 rows are rows 4jj .. 4jj+3 of each of the four 32-row groups of a scale atom's 128:
-//     their scales are 64 consecutive bytes per 64 columns, and in the gate/up interleaved pack
-//     groups 0, 1 are gate rows and groups 2, 3 the matching up rows, which land in one lane.
+//   - Activations are f16 with a power of two per token and stretch that brings the stretch's largest
+//     to [2^14, 2^15): x per 128 elements, which keeps every bf16 down to 2^-31 of the largest exact;
+//     h, kept with 11 bits, per 32.  The powers are taken out of a chunk's sum.
+//   - A scale atom's 16 bytes j hold the scales of rows j, 32 + j, 64 + j, 96 + j of its 128.  Tiles go in
+//     pairs over eight j: the first takes rows j and 64 + j, the second rows 32 + j and 96 + j, so that one
+//     16-byte load brings a lane the scales of both tiles.  In the gate/up interleaved pack rows 0 .. 63
+//     are gate rows and 64 .. 127 the matching up rows, which land in one lane.
+//   - The ring is filled by asynchronous copies, three steps ahead: a warp has six scoreboards for its
+//     loads, and a ring in registers waits for its youngest load with its oldest (measured: 3.6 TB/s
+//     without any arithmetic, at any depth).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -24,82 +29,74 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 4;       // warps of a gate_up block: they split K
-constexpr int kTiles = 4;       // 16-row tiles per gate_up item
-constexpr int kDnWarps = 8;     // warps of a down block: they split the (slot, K) list
-constexpr int kDnTiles = 4;
-constexpr int kDnRows = 16 * kDnTiles;
+constexpr int kSlot = 8;                        // tokens of a slot
+constexpr int kWarps = 16;                      // warps of a block, one block a SM
+constexpr int kTiles = 4;                       // 16-row tiles of a unit: two pairs
+constexpr int kSteps = 3;                       // depth of the ring; a step is a pair's 128 columns
+constexpr int kStepBytes = 4 * 512 + 256;       // codes: [4][32 lanes] x 16 bytes, scales: [16] x 16 bytes
+constexpr int kActBytes = 4 * 512 + 256;        // activations of a chunk: [4][32] x 16 bytes, scales [32] x 8
+constexpr int kWarpBytes = kSteps * kStepBytes + 2 * kActBytes;
+constexpr int kRedBytes = kTiles * 512;         // a warp's sums, for the warps that split K with it
+constexpr int kRingBytes = kWarps * (kWarpBytes + kRedBytes);
 
-// A slot is up to eight tokens (pairs) of one expert.  Workspace words: [0] slots n, then (expert,
-// first pair, end) x n from kListHead on, the pairs t * k + j in slot order, and one arrival count
-// per kDnRows output columns (zeroed by the gate_up kernel).
+// Workspace words: [0] slots n; a word per slot from kListHead on (expert, first pair << 10, count << 21);
+// token of each pair in slot order (bytes); place in slot order of pair t * k + j (-1: none); arrivals
+// per group of output columns.
 constexpr int kListHead = 16;
-constexpr int kFewMaxSlots = kMaxRouteExperts + kFewMaxPairs / 8;
-__host__ __device__ inline int max_slots(int P, int E) { return P < E + P / 8 ? P : E + P / 8; }
+__host__ __device__ inline int token_words(int P) { return (P + 3) / 4; }
+__host__ __device__ inline int list_tokens(int P) { return kListHead + P; }
+__host__ __device__ inline int list_places(int P) { return list_tokens(P) + token_words(P); }
+__host__ __device__ inline int list_arrived(int P) { return list_places(P) + P; }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {  // weights are read once
+// Asynchronous 16-byte copies; weights past L1, activations through it.
+__device__ __forceinline__ void copy16_stream(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t smem) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(smem) : "memory");
+  return r;
+}
+__device__ __forceinline__ float2 lds8(uint32_t smem) {
+  float2 r;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(smem) : "memory");
   return r;
 }
 
-// One 16 x 128 chunk of a tile as it is loaded: 32 codes of each of the lane's two rows and the
-// scales of their two 16-blocks.
-struct Chunk {
-  uint4 lo, hi;
-  uint16_t sl, sh;
-};
-
-// The lane's part of a tile of a packed matrix.
-struct TileRef {
-  const uint8_t* codes;  // the lane's low row, its 16 bytes of chunk 0
-  const uint8_t* sf;     // the lane's two scales of the low row, chunk 0; the high row's follow 8 bytes on
-};
-
-// Of a tile whose index is a multiple of 4; the three after it lie 4 rows and 64 scale bytes apart.
-__device__ __forceinline__ TileRef tile_ref(const uint8_t* codes, const uint8_t* sf, int tile, int cols) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int q = tile >> 3, j = 4 * (tile & 7) + (g & 3);
-  const int64_t row = 128 * (int64_t)q + 32 * (g >> 2) + j;
-  TileRef r;
-  r.codes = codes + row * (cols / 2) + 16 * t;
-  r.sf = sf + ((int64_t)q * (cols / 64) + (t >> 1)) * 512 + j * 16 + (g >> 2) * 4 + (t & 1) * 2;
-  return r;
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint16_t ldg_u16(const uint8_t* p) {
-  uint16_t r;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-  return r;
-}
-
-// Tile `r` after the reference; `in` false (past the last 64 columns): zeros.
-__device__ __forceinline__ Chunk load_chunk(const TileRef& ref, int r, int cols, bool in) {
-  Chunk k;
-  if (in) {
-    const uint8_t* p = ref.codes + r * (2 * cols);
-    k.lo = ldg_stream(p);
-    k.hi = ldg_stream(p + 32 * (int64_t)cols);
-    k.sl = ldg_u16(ref.sf + 64 * r);
-    k.sh = ldg_u16(ref.sf + 64 * r + 8);
-  } else {
-    k.lo = k.hi = make_uint4(0, 0, 0, 0);
-    k.sl = k.sh = 0;
-  }
-  return k;
-}
-
-// The byte `i` of a word of codes -> two halves.  The conversion reads its register's low byte.
+// The byte `I` of a word of codes -> two halves.  The conversion reads its register's low byte.
 template <int I>
 __device__ __forceinline__ uint32_t decode_byte(uint32_t w) {
   uint32_t r;
@@ -110,7 +107,6 @@ __device__ __forceinline__ uint32_t decode_byte(uint32_t w) {
       : "r"(w >> (8 * I)));
   return r;
 }
-
 __device__ __forceinline__ uint32_t scale_low(uint32_t a, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __low2half2(s));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -119,108 +115,60 @@ __device__ __forceinline__ uint32_t scale_high(uint32_t a, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(s));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-
-__device__ __forceinline__ __half2 e4m3x2(uint16_t c) {
+// The scales of the lane's two 16-blocks among the four of a word.
+__device__ __forceinline__ __half2 lane_scales(uint32_t w) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(w >> (16 * (threadIdx.x & 1)))));
   return *reinterpret_cast<const __half2*>(&r);
 }
 
-// acc += (chunk of weights) x (B fragments b of the same 128 elements), in units of the weights'
-// tensor scale and of the activations' scale.
-__device__ __forceinline__ void mma_chunk(float (&acc)[4], const Chunk& k, const uint32_t (&b)[16]) {
-  const __half2 sl = e4m3x2(k.sl), sh = e4m3x2(k.sh);
-  const uint32_t lo[4] = {k.lo.x, k.lo.y, k.lo.z, k.lo.w}, hi[4] = {k.hi.x, k.hi.y, k.hi.z, k.hi.w};
+// acc += d x (16 x 128 codes of a tile) x (B fragments b of the same 128 elements): lo, hi are the
+// lane's 32 codes of its low and high row, d0, d1 the scales taken out of the lane's two columns.
+__device__ __forceinline__ void mma_tile(float (&acc)[4], const uint4& klo, const uint4& khi, uint32_t sf_lo,
+                                         uint32_t sf_hi, const uint32_t (&b)[16], float d0, float d1) {
+  const __half2 sl = lane_scales(sf_lo), sh = lane_scales(sf_hi);
+  const uint32_t lo[4] = {klo.x, klo.y, klo.z, klo.w}, hi[4] = {khi.x, khi.y, khi.z, khi.w};
+  float part[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     // a word is 8 codes: the first two words belong to the lane's first 16-block
     auto sc = [&](uint32_t a, __half2 s) { return w < 2 ? scale_low(a, s) : scale_high(a, s); };
-    mma16816(acc, sc(decode_byte<0>(lo[w]), sl), sc(decode_byte<0>(hi[w]), sh), sc(decode_byte<1>(lo[w]), sl),
-             sc(decode_byte<1>(hi[w]), sh), b[4 * w], b[4 * w + 1]);
-    mma16816(acc, sc(decode_byte<2>(lo[w]), sl), sc(decode_byte<2>(hi[w]), sh), sc(decode_byte<3>(lo[w]), sl),
+    const uint32_t a0 = sc(decode_byte<0>(lo[w]), sl), a1 = sc(decode_byte<0>(hi[w]), sh);
+    const uint32_t a2 = sc(decode_byte<1>(lo[w]), sl), a3 = sc(decode_byte<1>(hi[w]), sh);
+    if (w == 0)
+      mma16816_first(part, a0, a1, a2, a3, b[0], b[1]);
+    else
+      mma16816(part, a0, a1, a2, a3, b[4 * w], b[4 * w + 1]);
+    mma16816(part, sc(decode_byte<2>(lo[w]), sl), sc(decode_byte<2>(hi[w]), sh), sc(decode_byte<3>(lo[w]), sl),
              sc(decode_byte<3>(hi[w]), sh), b[4 * w + 2], b[4 * w + 3]);
   }
+  acc[0] = fmaf(part[0], d0, acc[0]);
+  acc[1] = fmaf(part[1], d1, acc[1]);
+  acc[2] = fmaf(part[2], d0, acc[2]);
+  acc[3] = fmaf(part[3], d1, acc[3]);
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The power of two for a chunk whose largest magnitude is amax, and its inverse.
-__device__ __forceinline__ void chunk_scale(float amax, float* up, float* down) {
-  const int e = min(max((int)(__float_as_uint(amax) >> 23), 15), 254);
+// The power of two that brings a magnitude of binary32 exponent field e to [2^14, 2^15), and its
+// inverse times 2^-12: sums of weights in units of their tensor scale are up to 2^12 times the
+// result's size, and would overflow first.  2^12 comes back with the tensor scale.  Below 2^-100 the
+// largest power is taken; an infinity or NaN counts as 2^127.
+constexpr float kSumUnit = 4096.0f;
+__device__ __forceinline__ void stretch_scale(int e, float* up, float* down) {
+  e = min(max(e, 27), 254);
   *up = __uint_as_float((uint32_t)(268 - e) << 23);
-  *down = __uint_as_float((uint32_t)(e - 14) << 23);
+  *down = __uint_as_float((uint32_t)(e - 26) << 23);
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-
-__device__ __forceinline__ float max3_abs(float m, float a, float b) {
-  return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
-}
-
-// B fragments of 128 elements of the lane's column (token), and the scale taken out.
-__device__ __forceinline__ float scale_to_f16(const float (&v)[32], uint32_t (&b)[16]) {
-  float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    m0 = max3_abs(m0, v[i], v[i + 1]);
-    m1 = max3_abs(m1, v[i + 2], v[i + 3]);
-  }
-  float up, down;
-  chunk_scale(quad_max(fmaxf(m0, m1)), &up, &down);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) b[i] = pack_f16(v[2 * i] * up, v[2 * i + 1] * up);
-  return down;
-}
-
-// row: the lane's 32 elements of the chunk; `in` false: zeros
-__device__ __forceinline__ float load_b_bf16(const uint16_t* row, bool in, uint32_t (&b)[16]) {
-  float v[32];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (in) r = __ldg(reinterpret_cast<const uint4*>(row) + i);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-  return scale_to_f16(v, b);
-}
-
-__device__ __forceinline__ float load_b_f32(const float* row, bool in, uint32_t (&b)[16]) {
-  float v[32];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (in) r = __ldg(reinterpret_cast<const float4*>(row) + i);
-    v[4 * i] = r.x;
-    v[4 * i + 1] = r.y;
-    v[4 * i + 2] = r.z;
-    v[4 * i + 3] = r.w;
-  }
-  return scale_to_f16(v, b);
-}
-
-struct Lists {
-  uint16_t id[kFewMaxPairs];             // expert of pair t * k + j (0xFFFF: none)
-  uint16_t order[kFewMaxPairs];          // pairs in expert order, tokens ascending
+// ----------------------------------------------------------------------------------------
+// routing and layout
+// ----------------------------------------------------------------------------------------
+struct ListScratch {
+  uint16_t id[kFewMaxPairs];   // expert of pair t * k + j (0xFFFF: none)
   int cursor[kMaxRouteExperts];
-  uint16_t expert[kFewMaxSlots];         // slots, experts ascending
-  uint16_t start[kFewMaxSlots];          // first pair of each
-  uint8_t count[kFewMaxSlots];
-  int n, pairs;
 };
 
 // The same choice and weights as moe_route_topk: k rounds of a warp arg-max over ordered keys.
-__device__ void route_token(const MoeFewArgs& a, int t, uint16_t* id, bool write) {
+__device__ void route_token(const MoeFewArgs& a, int t, uint16_t* id) {
   const int lane = threadIdx.x & 31;
   const int nb = (a.E + 255) / 256;
   uint32_t key[8];
@@ -236,8 +184,8 @@ __device__ void route_token(const MoeFewArgs& a, int t, uint16_t* id, bool write
       }
     }
   };
-  if (nb == 1) load(0);
-  float lmax = 0.0f, sum = 0.0f, mine_p = 0.0f;
+  load(0);
+  uint32_t mine_key = 0;  // lane j keeps the j-th choice
   int mine_e = -1;
   bool bad = false;
   for (int j = 0; j < a.k; ++j) {
@@ -257,374 +205,419 @@ __device__ void route_token(const MoeFewArgs& a, int t, uint16_t* id, bool write
       bad = true;
       break;
     }
-    const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0x7FFFFFFFu);
+    const uint32_t have = __ballot_sync(0xffffffffu, best == top);
+    int e = __shfl_sync(0xffffffffu, be, __ffs(have) - 1);
+    if (have & (have - 1)) e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0x7FFFFFFFu);
     if ((e & 31) == lane) {
       const int i = (e >> 5) & 7;
+      if (nb > 1) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (b == e >> 8) taken[b] |= 1u << i;
+        for (int b = 0; b < 4; ++b)
+          if (b == e >> 8) taken[b] |= 1u << i;
+      } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q == i && nb == 1) key[q] = 0;
+        for (int q = 0; q < 8; ++q)
+          if (q == i) key[q] = 0;
+      }
     }
-    const float l = __uint_as_float((top & 0x80000000u) ? (top & 0x7FFFFFFFu) : ~top);
-    if (j == 0) lmax = l;
-    const float p = expf(__fsub_rn(l, lmax));
-    sum = __fadd_rn(sum, p);
     if (lane == j) {
-      mine_p = p;
+      mine_key = top;
       mine_e = e;
     }
   }
+  const float l = __uint_as_float((mine_key & 0x80000000u) ? (mine_key & 0x7FFFFFFFu) : ~mine_key);
+  const float p = expf(__fsub_rn(l, __shfl_sync(0xffffffffu, l, 0)));
+  float sum = 0.0f;
+  for (int j = 0; j < a.k; ++j) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, p, j));
   if (lane < a.k) {
-    const int p = t * a.k + lane;
-    id[p] = bad ? 0xFFFFu : (uint16_t)mine_e;
-    if (write) {
-      a.ids[p] = bad ? -1 : mine_e;
-      a.topk_w[p] = bad ? 0.0f : __fdiv_rn(mine_p, sum);
-    }
+    const int i = t * a.k + lane;
+    id[i] = bad ? 0xFFFFu : (uint16_t)mine_e;
+    a.ids[i] = bad ? -1 : mine_e;
+    a.topk_w[i] = bad ? 0.0f : __fdiv_rn(p, sum);
   }
-  if (bad && write && lane == 0) report_status(a.status, kErrRange);
+  if (bad && lane == 0) report_status(a.status, kErrRange);
 }
 
-// Every block routes all tokens itself: T k rounds of ~100 cycles over its warps against a launch
-// and a pass over memory.  Block 0 also writes the choice and the lists for the down kernel.
-__device__ void build_lists(const MoeFewArgs& a, Lists& L) {
+__device__ __forceinline__ uint32_t slot_word(int e, int first, int count) {
+  return (uint32_t)e | (uint32_t)first << 10 | (uint32_t)count << 21;
+}
+
+__device__ void build_lists(const MoeFewArgs& a, ListScratch& B) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int P = a.T * a.k;
-  const bool write = blockIdx.x == 0;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) L.cursor[e] = 0;
-  for (int t = warp; t < a.T; t += blockDim.x / 32) route_token(a, t, L.id, write);
+  uint32_t* slots = reinterpret_cast<uint32_t*>(a.lists + kListHead);
+  uint8_t* token = reinterpret_cast<uint8_t*>(a.lists + list_tokens(P));
+  int32_t* places = a.lists + list_places(P);
+  for (int i = threadIdx.x; i < a.H / 64; i += blockDim.x) a.lists[list_arrived(P) + i] = 0;
+  if (P > 32)
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) B.cursor[e] = 0;
+  for (int t = warp; t < a.T; t += blockDim.x / 32) route_token(a, t, B.id);
   __syncthreads();
-  for (int p = threadIdx.x; p < P; p += blockDim.x)
-    if (L.id[p] != 0xFFFFu) atomicAdd(&L.cursor[L.id[p]], 1);
-  __syncthreads();
-  if (warp == 0) {
-    int n = 0, at = 0;  // slots and pairs before this group of experts
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int cnt = e < a.E ? L.cursor[e] : 0;
-      if (__ballot_sync(0xffffffffu, cnt > 0) == 0) continue;
-      int run = cnt | (cnt + 7) / 8 << 16;  // pairs low, slots high
-      const int own = run;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
-      }
-      const int first = at + ((run - own) & 0xFFFF);
-      int i = n + ((run - own) >> 16);
-      for (int c = 0; c < cnt; c += 8, ++i) {
-        L.expert[i] = (uint16_t)e;
-        L.start[i] = (uint16_t)(first + c);
-        L.count[i] = (uint8_t)min(8, cnt - c);
-      }
-      if (cnt > 0) L.cursor[e] = first;
-      const int all = __shfl_sync(0xffffffffu, run, 31);
-      at += all & 0xFFFF;
-      n += all >> 16;
+  if (P <= 32) {
+    // one warp sorts the pairs by expert: a pair's place is the number of those before it
+    if (warp != 0) return;
+    const uint32_t e = lane < P ? B.id[lane] : 0xFFFFu;
+    int place = 0, rank = 0;
+    for (int j = 0; j < P; ++j) {
+      const uint32_t ej = __shfl_sync(0xffffffffu, e, j);
+      const bool before = ej == e && j < lane;
+      rank += before;
+      place += before || ej < e;
     }
-    if (lane == 0) {
-      L.n = n;
-      L.pairs = at;
-    }
-    __syncwarp();
-    // ranks in pair order, 32 at a time
-    for (int p0 = 0; p0 < P; p0 += 32) {
-      const int p = p0 + lane;
-      const uint32_t e = p < P ? L.id[p] : 0xFFFFu;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const uint32_t before = __popc(same & ((1u << lane) - 1u));
-      int base = 0;
-      if (e != 0xFFFFu) base = L.cursor[e];
-      __syncwarp();
-      if (e != 0xFFFFu) {
-        L.order[base + before] = (uint16_t)p;
-        if (before == 0) L.cursor[e] = base + __popc(same);
-      }
-      __syncwarp();
-    }
+    const int cnt = __popc(__match_any_sync(0xffffffffu, e));
+    if (e != 0xFFFFu) token[place] = (uint8_t)(lane / a.k);
+    if (lane < P) places[lane] = e != 0xFFFFu ? place : -1;
+    // slots in the order of places: a slot's first pair has a rank that is a multiple of its size
+    const bool first = e != 0xFFFFu && rank % kSlot == 0;
+    int i = 0;
+    for (int j = 0; j < P; ++j) i += __shfl_sync(0xffffffffu, first ? place : 64, j) < place;
+    if (first) slots[i] = slot_word((int)e, place, min(kSlot, cnt - rank));
+    const int n = __popc(__ballot_sync(0xffffffffu, first));
+    if (lane == 0) a.lists[0] = n;
+    return;
   }
+  for (int p = threadIdx.x; p < P; p += blockDim.x)
+    if (B.id[p] != 0xFFFFu) atomicAdd(&B.cursor[B.id[p]], 1);
   __syncthreads();
-  if (write) {
-    const int n = L.n;
-    int32_t* o = a.lists;
-    if (threadIdx.x == 0) o[0] = n;
-    o += kListHead;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      o[3 * i] = L.expert[i];
-      o[3 * i + 1] = L.start[i];
-      o[3 * i + 2] = L.start[i] + L.count[i];
+  if (warp != 0) return;
+  int n = 0, at = 0;  // slots and pairs before this group of experts
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    const int cnt = e < a.E ? B.cursor[e] : 0;
+    if (__ballot_sync(0xffffffffu, cnt > 0) == 0) continue;
+    int run = cnt | (cnt + kSlot - 1) / kSlot << 16;  // pairs low, slots high
+    const int own = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
     }
-    o += 3 * max_slots(P, a.E);
-    for (int p = threadIdx.x; p < L.pairs; p += blockDim.x) o[p] = L.order[p];
-    o += P;
-    for (int i = threadIdx.x; i < a.H / kDnRows; i += blockDim.x) o[i] = 0;
+    const int first = at + ((run - own) & 0xFFFF);
+    int i = n + ((run - own) >> 16);
+    for (int c = 0; c < cnt; c += kSlot, ++i) slots[i] = slot_word(e, first + c, min(kSlot, cnt - c));
+    if (cnt > 0) B.cursor[e] = first;
+    const int all = __shfl_sync(0xffffffffu, run, 31);
+    at += all & 0xFFFF;
+    n += all >> 16;
+  }
+  if (lane == 0) a.lists[0] = n;
+  __syncwarp();
+  // ranks in pair order, 32 at a time
+  for (int p0 = 0; p0 < P; p0 += 32) {
+    const int p = p0 + lane;
+    const uint32_t e = p < P ? B.id[p] : 0xFFFFu;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    int base = 0;
+    if (e != 0xFFFFu) base = B.cursor[e];
+    __syncwarp();
+    if (e != 0xFFFFu) {
+      token[base + before] = (uint8_t)(p / a.k);
+      if (before == 0) B.cursor[e] = base + __popc(same);
+    }
+    if (p < P) places[p] = e != 0xFFFFu ? base + before : -1;
+    __syncwarp();
   }
 }
 
 }  // namespace
 
-// gate_up + SwiGLU.  An item is (slot, kTiles tiles); a block's warps split its K in interleaved
-// chunks and join their sums in shared memory, in warp order.  Each warp keeps the next chunk of
-// every tile in flight, across the end of an item too.
-__global__ void __launch_bounds__(kWarps * 32, 4) moe_few_gate_up_kernel(MoeFewArgs a) {
-  __shared__ Lists L;
-  __shared__ float red[kWarps][kTiles][16][8];
-  build_lists(a, L);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int groups = a.I / 8 / kTiles;
-  const int nch = a.H / 128;
-  const int items = L.n * groups;
-  const int64_t cb = (int64_t)a.I * a.H, sb = (int64_t)a.I * a.H / 8;  // bytes of one expert's codes / scales
-  auto item_ref = [&](int it) {
-    const int64_t e = L.expert[it / groups];
-    TileRef r = tile_ref(a.gu_codes + e * cb, a.gu_sf + e * sb, it % groups * kTiles, a.H);
-    r.codes += 64 * warp;
-    r.sf += 1024 * warp;
-    return r;
-  };
-  int it = blockIdx.x;
-  if (it >= items) return;
-  TileRef next = item_ref(it);  // what the ring holds or is about to
-  Chunk ring[kTiles];
-  const bool any = warp < nch;
-#pragma unroll
-  for (int r = 0; r < kTiles; ++r) ring[r] = load_chunk(next, r, a.H, any);
-  for (; it < items; it += gridDim.x) {
-    const int slot = it / groups;
-    const int p0 = L.start[slot], cnt = L.count[slot];
-    const float s_g = __ldg(a.gu_sg + L.expert[slot]);
-    const bool has = g < cnt;
-    const uint16_t* xr = a.x + (has ? (int64_t)(L.order[p0 + g] / a.k) * a.ldx : 0) + 32 * t;
-    float acc[kTiles][4] = {};
-    for (int c = warp; c < nch; c += kWarps) {
-      bool more = true;
-      if (c + kWarps < nch) {
-        next.codes += 64 * kWarps;
-        next.sf += 1024 * kWarps;
-      } else if (it + gridDim.x < items) {
-        next = item_ref(it + gridDim.x);
-      } else {
-        more = false;
-      }
-      uint32_t b[16];
-      const float down = load_b_bf16(xr + 128 * c, has, b) * s_g;
-      const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-      for (int r = 0; r < kTiles; ++r) {
-        const Chunk k = ring[r];
-        if (more) ring[r] = load_chunk(next, r, a.H, true);
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_chunk(part, k, b);
-        acc[r][0] = fmaf(part[0], d0, acc[r][0]);
-        acc[r][1] = fmaf(part[1], d1, acc[r][1]);
-        acc[r][2] = fmaf(part[2], d0, acc[r][2]);
-        acc[r][3] = fmaf(part[3], d1, acc[r][3]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kTiles; ++r) {
-      *reinterpret_cast<float2*>(&red[warp][r][g][2 * t]) = make_float2(acc[r][0], acc[r][1]);
-      *reinterpret_cast<float2*>(&red[warp][r][g + 8][2 * t]) = make_float2(acc[r][2], acc[r][3]);
-    }
-    __syncthreads();
-    for (int o = threadIdx.x; o < kTiles * 64; o += kWarps * 32) {
-      const int col = o >> 5, r = (o >> 3) & 3, row = o & 7;
-      if (col < cnt) {
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gate += red[w][r][row][col];
-          up += red[w][r][row + 8][col];
-        }
-        const int tile = it % groups * kTiles + r;
-        const int hi = 64 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
-        a.h[(int64_t)(p0 + col) * a.I + hi] = gate / (1.0f + expf(-gate)) * up;
-      }
-    }
-    __syncthreads();
+// The last block routes and lays out the slots; block t converts row t of x to f16, a warp per chunk.
+__global__ void __launch_bounds__(1024) moe_few_prepare_kernel(MoeFewArgs a) {
+  __shared__ ListScratch scratch;
+  if ((int)blockIdx.x == a.T) {
+    build_lists(a, scratch);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  for (int c = warp; c < a.H / 128; c += 32) {
+    const uint2 r = __ldg(reinterpret_cast<const uint2*>(a.x + t * a.ldx + 128 * c) + lane);
+    const uint32_t m2 = __vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+    float up, down;
+    stretch_scale((int)(m >> 7), &up, &down);
+    uint2 o;
+    o.x = pack_f16(__uint_as_float(r.x << 16) * up, __uint_as_float(r.x & 0xFFFF0000u) * up);
+    o.y = pack_f16(__uint_as_float(r.y << 16) * up, __uint_as_float(r.y & 0xFFFF0000u) * up);
+    reinterpret_cast<uint2*>(a.xh + t * a.H + 128 * c)[lane] = o;
+    if (lane == 0) a.x_scale[t * (a.H / 128) + c] = down;
   }
 }
 
-// down + combine.  The units (kDnRows output columns, slot), columns outermost, are split evenly over
-// the blocks, so that few tokens still fill the card and many leave no last wave; a block's warps
-// split the (slot, chunk) list of each stretch, each adding w_tj * sum into a private [T][kDnRows]
-// array, joined in warp order.  Columns that several blocks share go through the workspace: the last
-// of these blocks to arrive adds their parts, in block order, so the result does not depend on timing.
-__global__ void __launch_bounds__(kDnWarps * 32, 2) moe_few_down_kernel(MoeFewArgs a) {
-  extern __shared__ float accw[];  // [kDnWarps][T][kDnRows]
-  __shared__ int last;
+// UP: gate_up + SwiGLU -> h.  Otherwise down: the products of each (slot, group of 64 output columns) go
+// to y in binary32, and the last warp to arrive at a group adds the pairs of every token in order of j:
+// the result does not depend on timing.
+//
+// Units are split evenly over the teams of S warps, in one contiguous run each (gate_up: slots outermost;
+// down: columns outermost, so that groups complete all along).  S is the least power of two that gives
+// every warp two units' worth of work, so that the last ones do not leave the card idle for long; a
+// team's warps take every S-th chunk and join in shared memory.
+template <bool UP>
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int P = a.T * a.k;
+  const int cols = UP ? a.H : a.I;                          // of the matrix
+  const int groups = UP ? a.I / 32 : a.H / 64;              // units per slot
+  const int nch = (cols + 127) / 128;
+  const int64_t cb = (int64_t)a.H * a.I / (UP ? 1 : 2), sb = cb / 8;  // bytes of one expert's codes / scales
+  const uint8_t* codes = UP ? a.gu_codes : a.dn_codes;
+  const uint8_t* sfs = UP ? a.gu_sf : a.dn_sf;
+  const float* s_gs = UP ? a.gu_sg : a.dn_sg;
+
+  uint32_t* slots = reinterpret_cast<uint32_t*>(smem + kRingBytes);
+  uint8_t* token = reinterpret_cast<uint8_t*>(slots + P);
   const int n = a.lists[0];
-  const int32_t* list = a.lists + kListHead;
-  const int32_t* order = list + 3 * max_slots(P, a.E);
-  int32_t* arrived = a.lists + kListHead + 3 * max_slots(P, a.E) + P;
-  const int nch = (a.I + 127) / 128;
-  const int64_t cb = (int64_t)a.H * a.I / 2, sb = (int64_t)a.H * a.I / 16;
-  const int elems = a.T * kDnRows;
-  const int groups = a.H / kDnRows;
-  auto store = [&](int grp, int i, float v) {
-    const int row = i % 16, tile = grp * kDnTiles + i % kDnRows / 16;
-    const int col = 128 * (tile >> 3) + 32 * (row >> 2) + 4 * (tile & 7) + (row & 3);
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    a.out[(int64_t)(i / kDnRows) * a.ldo + col] = *reinterpret_cast<const uint16_t*>(&b);
-  };
-  if (n == 0) {  // no token could be routed
-    for (int grp = blockIdx.x; grp < groups; grp += gridDim.x)
-      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) store(grp, i, 0.0f);
+  for (int i = threadIdx.x; i < P; i += kWarps * 32) slots[i] = (uint32_t)a.lists[kListHead + i];
+  if (UP)
+    for (int i = threadIdx.x; i < token_words(P); i += kWarps * 32)
+      reinterpret_cast<uint32_t*>(token)[i] = (uint32_t)a.lists[list_tokens(P) + i];
+  __syncthreads();
+
+  if (!UP && n == 0) {  // no token could be routed
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)a.T * a.H; i += (int64_t)gridDim.x * blockDim.x)
+      a.out[i / a.H * a.ldo + i % a.H] = 0;
     return;
   }
-  const int64_t units = (int64_t)groups * n;
-  const int64_t G = min((int64_t)gridDim.x, units);
-  if (blockIdx.x >= G) return;
-  auto bound = [&](int64_t b) { return units * b / G; };                       // first unit of block b
-  auto block_of = [&](int64_t u) { return ((u + 1) * G - 1) / units; };        // the block that holds unit u
-  int64_t u = bound(blockIdx.x);
-  const int64_t u_end = bound(blockIdx.x + 1);
-  float* mine = accw + warp * elems;
-  for (int part = 0; u < u_end; ++part) {
-    const int grp = (int)(u / n);
-    const int s_lo = (int)(u - (int64_t)grp * n);
-    const int s_hi = (int)min((int64_t)n, s_lo + (u_end - u));
-    u += s_hi - s_lo;
-    for (int i = lane; i < elems; i += 32) mine[i] = 0.0f;
-    __syncwarp();
-    const int todo = (s_hi - s_lo) * nch;
-    int w0 = todo * warp / kDnWarps;
-    const int w1 = todo * (warp + 1) / kDnWarps;
-    int slot = s_lo + w0 / nch, c = w0 % nch;
-    auto slot_ref = [&](int sl, int ch) {
-      const int64_t e = __ldg(list + 3 * sl);
-      TileRef r = tile_ref(a.dn_codes + e * cb, a.dn_sf + e * sb, grp * kDnTiles, a.I);
-      r.codes += 64 * ch;
-      r.sf += 1024 * ch;
-      return r;
-    };
-    TileRef next;
-    Chunk ring[kDnTiles];
-    if (w0 < w1) {
-      next = slot_ref(slot, c);
+  const int units = n * groups;
+  const int warps = gridDim.x * kWarps;
+  int S = 1;
+  while (S < kWarps && 2 * S <= nch && units * S < 2 * warps) S *= 2;
+  const int team = (blockIdx.x * kWarps + warp) / S, teams = warps / S, part = warp & (S - 1);
+  int u = (int)((int64_t)units * team / teams);
+  const int u_end = (int)((int64_t)units * (team + 1) / teams);
+  if (u >= u_end) return;  // a team's warps agree
+
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem) + warp * kWarpBytes;
+  const uint32_t acts = base + kSteps * kStepBytes;
+  const int my_chunks = (nch - part + S - 1) / S;  // at least one: S <= nch
+
+  // ---- the copying side, kSteps steps ahead
+  int cu = u, cc = 0, cpair = 0;  // unit, chunk (of this warp's), pair
+  uint32_t cstep = 0, cact = 0;   // offsets of the ring's next places
+  const uint8_t *pc = nullptr, *ps = nullptr;
+  const uint8_t *pa = nullptr, *pas = nullptr;  // the lane's activations of chunk 0, their scales
+  bool col = false;
+  auto enter = [&](int unit) {
+    const int slot = UP ? unit / groups : unit % n, grp = UP ? unit % groups : unit / n;
+    const uint32_t w = slots[slot];
+    const int64_t e = w & 1023u;
+    const int first = (int)(w >> 10 & 2047u), cnt = (int)(w >> 21);
+    // pairs of tiles 2 grp, 2 grp + 1 of the matrix's, four to 128 rows: rows j, j + 8 .. of each 32
+    const int j = 16 * (grp & 1) + g;
+    pc = codes + e * cb + (128 * (int64_t)(grp >> 1) + j) * (cols / 2) + 16 * t + 64 * part;
+    ps = sfs + e * sb + ((int64_t)(grp >> 1) * (cols / 64) + (t >> 1)) * 512 + j * 16 + 1024 * part;
+    col = g < cnt;
+    const int64_t r = UP ? (col ? token[first + g] : 0) : first + (col ? g : 0);
+    pa = reinterpret_cast<const uint8_t*>(UP ? a.xh : a.h) + (r * cols + 32 * t + 128 * part) * 2;
+    pas = reinterpret_cast<const uint8_t*>(UP ? a.x_scale + r * (cols / 128) + part
+                                              : a.h_scale + r * (cols / 32) + 2 * (t >> 1) + 4 * part);
+  };
+  auto copy_step = [&]() {
+    if (cu < u_end) {
+      const int k0 = 128 * (part + S * cc);
+      // past the last 64 columns the lane reads those before them, against activations of zero
+      const bool in = UP || k0 + 32 * t < cols;
+      const uint8_t* q = pc + (in ? 0 : -32);
+      const uint32_t dst = base + cstep;
+      const int64_t row8 = 4 * (int64_t)cols;  // bytes of eight rows
+      copy16_stream(dst + 16 * lane, q);
+      copy16_stream(dst + 16 * lane + 512, q + 4 * row8);
+      copy16_stream(dst + 16 * lane + 1024, q + 8 * row8);
+      copy16_stream(dst + 16 * lane + 1536, q + 12 * row8);
+      if ((t & 1) == 0) copy16_stream(dst + 2048 + 32 * g + 8 * t, ps + (in ? 0 : -512));
+      if (cpair == 0) {
+        if (col && in) {
+          const uint32_t adst = acts + cact;
 #pragma unroll
-      for (int r = 0; r < kDnTiles; ++r) ring[r] = load_chunk(next, r, a.I, 128 * c + 32 * t < a.I);
-    }
-    while (w0 < w1) {
-      const int c_end = min(nch, c + (w1 - w0));
-      const int p0 = __ldg(list + 3 * slot + 1), cnt = __ldg(list + 3 * slot + 2) - p0;
-      const float s_g = __ldg(a.dn_sg + __ldg(list + 3 * slot));
-      const bool has = g < cnt;
-      const float* hr = a.h + (int64_t)(has ? p0 + g : 0) * a.I + 32 * t;
-      float acc[kDnTiles][4] = {};
-      w0 += c_end - c;
-      for (; c < c_end; ++c) {
-        bool more = true;
-        int cn = c + 1;
-        if (cn < c_end) {
-          next.codes += 64;
-          next.sf += 1024;
-        } else if (w0 < w1) {
-          next = slot_ref(slot + 1, 0);
-          cn = 0;
-        } else {
-          more = false;
+          for (int i = 0; i < 4; ++i) copy16(adst + 512 * i + 16 * lane, pa + 16 * i);
+          if (UP)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(adst + 2048 + 8 * lane), "l"(pas) : "memory");
+          else
+            copy8(adst + 2048 + 8 * lane, pas);
         }
-        const bool in = 128 * c + 32 * t < a.I, in_next = more && 128 * cn + 32 * t < a.I;
-        uint32_t b[16];
-        const float down = load_b_f32(hr + 128 * c, has && in, b) * s_g;
-        const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        cact ^= kActBytes;
+        cpair = 1;
+        pc += row8;
+        ps += 128;
+      } else {
+        cpair = 0;
+        ++cc;
+        pc += 64 * S - row8;
+        ps += 1024 * S - 128;
+        pa += 256 * S;
+        pas += (UP ? 4 : 16) * S;
+        if (cc == my_chunks) {
+          cc = 0;
+          if (++cu < u_end) enter(cu);
+        }
+      }
+      cstep = cstep == (kSteps - 1) * kStepBytes ? 0 : cstep + kStepBytes;
+    }
+    copies_commit();
+  };
+  enter(u);
 #pragma unroll
-        for (int r = 0; r < kDnTiles; ++r) {
-          const Chunk k = ring[r];
-          ring[r] = load_chunk(next, r, a.I, in_next);
-          float pt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_chunk(pt, k, b);
-          acc[r][0] = fmaf(pt[0], d0, acc[r][0]);
-          acc[r][1] = fmaf(pt[1], d1, acc[r][1]);
-          acc[r][2] = fmaf(pt[2], d0, acc[r][2]);
-          acc[r][3] = fmaf(pt[3], d1, acc[r][3]);
+  for (int i = 0; i < kSteps; ++i) copy_step();
+
+  uint32_t step = 0, act = 0;
+  float* red = reinterpret_cast<float*>(smem + kWarps * kWarpBytes);
+  for (; u < u_end; ++u) {
+    const int slot = UP ? u / groups : u % n, grp = UP ? u % groups : u / n;
+    const uint32_t w = slots[slot];
+    const int first = (int)(w >> 10 & 2047u), cnt = (int)(w >> 21);
+    const float s_g = __ldg(s_gs + (w & 1023u)) * kSumUnit;
+    float acc[kTiles][4] = {};
+    for (int i = 0; i < my_chunks; ++i) {
+      uint32_t b[16] = {};
+      float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+      for (int pr = 0; pr < 2; ++pr) {
+        copies_wait<kSteps - 1>();
+        __syncwarp();  // the scales of a row are copied by one lane and read by two
+        const uint32_t src = base + step;
+        const uint4 lo0 = lds16(src + 16 * lane), lo1 = lds16(src + 16 * lane + 512);
+        const uint4 hi0 = lds16(src + 16 * lane + 1024), hi1 = lds16(src + 16 * lane + 1536);
+        const uint4 sf = lds16(src + 2048 + 32 * g + 16 * (t >> 1));
+        if (pr == 0) {
+          const bool in = UP || 128 * (part + S * i) + 32 * t < cols;
+          float2 f = make_float2(0.0f, 0.0f);
+          if (g < cnt && in) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(acts + act + 512 * q + 16 * lane);
+            f = lds8(acts + act + 2048 + 8 * lane);
+          }
+          float d = f.x;
+          if (!UP) {
+            // one scale per column and chunk: the largest; the others' elements take the quotient (a power
+            // of two).  Of the lane's 32 elements the first and the second 16 have a scale each.
+            d = fmaxf(fmaxf(f.x, f.y), 1.17549435e-38f);
+            d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
+            d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2));
+            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(d));
+            const uint32_t q0 = pack_f16(f.x * inv, f.x * inv), q1 = pack_f16(f.y * inv, f.y * inv);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) b[q] = hmul2(b[q], q < 8 ? q0 : q1);
+          }
+          d0 = __shfl_sync(0xffffffffu, d, 8 * t);
+          d1 = __shfl_sync(0xffffffffu, d, 8 * t + 4);
+          act ^= kActBytes;
+        }
+        mma_tile(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0, d1);
+        mma_tile(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0, d1);
+        step = step == (kSteps - 1) * kStepBytes ? 0 : step + kStepBytes;
+        __syncwarp();  // every lane has read the place that is filled next
+        copy_step();
+      }
+    }
+    if (S > 1) {
+      float4* mine = reinterpret_cast<float4*>(red + warp * (kRedBytes / 4)) + lane;
+      const int id = 1 + warp / S;
+      if (part != 0) {
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r) mine[32 * r] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * S) : "memory");
+      if (part == 0) {
+        for (int q = 1; q < S; ++q) {
+#pragma unroll
+          for (int r = 0; r < kTiles; ++r) {
+            const float4 v = mine[q * (kRedBytes / 16) + 32 * r];
+            acc[r][0] += v.x;
+            acc[r][1] += v.y;
+            acc[r][2] += v.z;
+            acc[r][3] += v.w;
+          }
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * S) : "memory");
+      if (part != 0) continue;
+    }
+    if (UP) {
+      // a unit's 32 rows of h are one scale stretch of each column
+      float h[kTiles][2], m[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int r = 0; r < kTiles; ++r) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float gate = acc[r][j] * s_g, up = acc[r][2 + j] * s_g;
+          h[r][j] = gate / (1.0f + expf(-gate)) * up;
+          // as integers, magnitudes keep their order and NaN is the largest
+          m[j] = __uint_as_float(max(__float_as_uint(m[j]), __float_as_uint(h[r][j]) & 0x7FFFFFFFu));
         }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int col = 2 * t + j;
-        if (col < cnt) {
-          const int p = __ldg(order + p0 + col);
-          const float w = __ldg(a.topk_w + p);
-          float* o = mine + (p / a.k) * kDnRows + g;  // a slot's tokens are distinct: no two lanes meet
+        uint32_t top = __float_as_uint(m[j]);
 #pragma unroll
-          for (int r = 0; r < kDnTiles; ++r) {
-            o[16 * r] = fmaf(w, acc[r][j], o[16 * r]);
-            o[16 * r + 8] = fmaf(w, acc[r][2 + j], o[16 * r + 8]);
-          }
+        for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float up, down;
+        stretch_scale((int)(top >> 23), &up, &down);
+        if (2 * t + j < cnt) {
+          const int64_t p = first + 2 * t + j;
+          uint16_t* o = a.h + p * a.I + 64 * (grp >> 1) + 16 * (grp & 1) + g;
+#pragma unroll
+          for (int r = 0; r < kTiles; ++r)
+            o[32 * (r & 1) + 8 * (r >> 1)] = __half_as_ushort(__float2half_rn(h[r][j] * up));
+          if (g == 0) a.h_scale[p * (a.I / 32) + grp] = down;
         }
-      }
-      __syncwarp();
-      ++slot;
-      c = 0;
-    }
-    __syncthreads();
-    const int64_t b0 = block_of((int64_t)grp * n), b1 = block_of((int64_t)grp * n + n - 1);
-    if (b0 == b1) {
-      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
-        float v = 0.0f;
-        for (int w = 0; w < kDnWarps; ++w) v += accw[w * elems + i];
-        store(grp, i, v);
       }
     } else {
-      // a block shares at most two groups of columns: the one that it enters in the middle (or
-      // before its end) and the one that it leaves unfinished
-      float* slot_out = a.partial + ((int64_t)blockIdx.x * 2 + (part > 0)) * elems;
-      for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
-        float v = 0.0f;
-        for (int w = 0; w < kDnWarps; ++w) v += accw[w * elems + i];
-        __stcg(slot_out + i, v);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (2 * t + j < cnt) {
+          float* o = a.y + (int64_t)(first + 2 * t + j) * a.H + 128 * (grp >> 1) + 16 * (grp & 1) + g;
+#pragma unroll
+          for (int r = 0; r < kTiles; ++r) {
+            __stcg(o + 32 * (r & 1) + 8 * (r >> 1), acc[r][j] * s_g);
+            __stcg(o + 64 + 32 * (r & 1) + 8 * (r >> 1), acc[r][2 + j] * s_g);
+          }
+        }
       }
       __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) last = atomicAdd(arrived + grp, 1) == (int)(b1 - b0);
-      __syncthreads();
-      if (last) {
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) last = atomicAdd(a.lists + list_arrived(P) + grp, 1) == n - 1;
+      if (__shfl_sync(0xffffffffu, last, 0)) {
         __threadfence();
-        for (int i = threadIdx.x; i < elems; i += kDnWarps * 32) {
-          float v = 0.0f;
-          for (int64_t b = b0; b <= b1; ++b) {
-            // block b's part of this group: its first stretch, or its second where it began before
-            const bool second = bound(b) < (int64_t)grp * n;
-            v += __ldcg(a.partial + (b * 2 + second) * elems + i);
+        // the group's 64 columns: four stretches of 16, two columns a lane
+        const int c = 128 * (grp >> 1) + 16 * (grp & 1) + 32 * (lane >> 3) + 2 * (lane & 7);
+        const int32_t* place = a.lists + list_places(P);
+#pragma unroll 4
+        for (int tok = 0; tok < a.T; ++tok) {
+          float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+          for (int j = 0; j < a.k; ++j) {
+            const int p = place[tok * a.k + j];
+            if (p >= 0) {
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(a.y + (int64_t)p * a.H + c));
+              const float wt = a.topk_w[tok * a.k + j];
+              v.x = fmaf(wt, y.x, v.x);
+              v.y = fmaf(wt, y.y, v.y);
+            }
           }
-          store(grp, i, v);
+          *reinterpret_cast<__nv_bfloat162*>(a.out + tok * a.ldo + c) = __floats2bfloat162_rn(v.x, v.y);
         }
       }
     }
-    __syncthreads();
   }
 }
 
-size_t moe_few_list_words(int64_t T, int32_t k, int32_t E, int64_t H) {
-  const int P = (int)(T * k);
-  return (size_t)(kListHead + 3 * max_slots(P, E) + P + H / kDnRows);
-}
-
-constexpr int kDnMaxBlocks = 2 * 160;
-size_t moe_few_partial_floats(int64_t T) { return (size_t)kDnMaxBlocks * 2 * (size_t)T * kDnRows; }
+size_t moe_few_list_words(int64_t T, int32_t k, int64_t H) { return (size_t)(list_arrived((int)(T * k)) + H / 64); }
 
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st) {
   const int P = a.T * a.k;
-  const int64_t slots = max_slots(P, a.E);
-  const int64_t items = slots * (a.I / 8 / kTiles), room = 4 * (int64_t)num_sms;
-  moe_few_gate_up_kernel<<<(unsigned)(items < room ? items : room), kWarps * 32, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int smem = kDnWarps * a.T * kDnRows * (int)sizeof(float);
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(moe_few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = kRingBytes + P * 4 + token_words(P) * 4;
+  static_assert(kRingBytes + kFewMaxPairs * 5 <= 227 * 1024, "the most pairs fit");
+  for (const void* f : {reinterpret_cast<const void*>(moe_few_stream_kernel<true>),
+                        reinterpret_cast<const void*>(moe_few_stream_kernel<false>)}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  int64_t blocks = slots * (a.H / kDnRows);
-  if (blocks > 2 * (int64_t)num_sms) blocks = 2 * (int64_t)num_sms;
-  if (blocks > kDnMaxBlocks) blocks = kDnMaxBlocks;
-  moe_few_down_kernel<<<(unsigned)blocks, kDnWarps * 32, smem, st>>>(a);
+  moe_few_prepare_kernel<<<a.T + 1, 1024, 0, st>>>(a);
+  moe_few_stream_kernel<true><<<num_sms, kWarps * 32, smem, st>>>(a);
+  moe_few_stream_kernel<false><<<num_sms, kWarps * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 

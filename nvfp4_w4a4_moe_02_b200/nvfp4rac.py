@@ -107,7 +107,7 @@ def load() -> ctypes.CDLL:
         "moe_row_pairs": ([vp, i64, i32, i64, vp, vp, vp], ctypes.c_int),
         "grouped_w4a4_rac_moe_combine": ([tp, tp, vp, vp, i32, tp, tp, i64, i64, i32, vp, vp, i64, i32, vp, vp, i64,
                                           vp, vp], ctypes.c_int),
-        "moe_w4a16_workspace_size": ([i64, i32, i32, i64, i64], sz),
+        "moe_w4a16_workspace_size": ([i64, i32, i64, i64], sz),
         "moe_w4a16_layer": ([vp, i64, i64, vp, i32, tp, tp, vp, vp, vp, i64, vp, sz, vp, vp], ctypes.c_int),
         "token_logprobs": ([vp, ctypes.c_int, i64, i64, i64, vp, i32, ctypes.c_float, i32, vp, vp, vp, vp, vp, vp, vp],
                            ctypes.c_int),
@@ -734,7 +734,7 @@ def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Pa
         w = torch.empty(T, k, dtype=torch.float32, device=dev) if w is None else w
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
         if workspace is None:
-            workspace = torch.empty(lib.moe_w4a16_workspace_size(T, k, E, H, I), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(lib.moe_w4a16_workspace_size(T, k, H, I), dtype=torch.uint8, device=dev)
         gu, dn = w_gate_up.c(), w_down.c()
         _check(lib.moe_w4a16_layer(x.data_ptr(), T, x.stride(0) if T > 1 else H, logits.data_ptr(), k,
                                    ctypes.byref(gu), ctypes.byref(dn), ids.data_ptr(), w.data_ptr(), out.data_ptr(),

@@ -191,7 +191,7 @@ def test_pitches_and_buffers_around_the_rows(dev):
 def test_workspace_is_not_written_past_its_size(dev):
     T, k, E, I = 5, 3, 6, 192
     x, logits, pgu, pdn = make_layer(dev, T, 384, I, E, k, seed=18)
-    n = R.load().moe_w4a16_workspace_size(T, k, E, 384, I)
+    n = R.load().moe_w4a16_workspace_size(T, k, 384, I)
     ws = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device=dev)
     ref = R.moe_w4a16_layer(x, logits, k, pgu, pdn)[0]
     out = R.moe_w4a16_layer(x, logits, k, pgu, pdn, workspace=ws[:n])[0]

@@ -51,9 +51,9 @@ def test_layer_without_tokens_needs_no_device(lib):
 
 
 def test_layer_workspace_size(lib):
-    assert lib.moe_w4a16_workspace_size(0, 2, 4, 256, 128) == 0
-    assert lib.moe_w4a16_workspace_size(64, 8, 256, 7168, 2048) >= 512 * 2048 * 2
-    assert lib.moe_w4a16_workspace_size(2, 2, 4, 256, 128) < lib.moe_w4a16_workspace_size(3, 2, 4, 256, 128)
+    assert lib.moe_w4a16_workspace_size(0, 2, 256, 128) == 0
+    assert lib.moe_w4a16_workspace_size(64, 8, 7168, 2048) >= 512 * 2048 * 2
+    assert lib.moe_w4a16_workspace_size(2, 2, 256, 128) < lib.moe_w4a16_workspace_size(3, 2, 256, 128)
 
 
 def fwd(**kw):
