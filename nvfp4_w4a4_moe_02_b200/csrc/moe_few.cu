@@ -159,6 +159,11 @@ __device__ __forceinline__ void stretch_scale(int e, float* up, float* down) {
   *down = __uint_as_float((uint32_t)(e - 26) << 23);
 }
 
+// The three kernels of a call overlap their launches: a kernel lets the next one start at once, and
+// that one waits here until this one's results are complete.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------------------
 // routing and layout
 // ----------------------------------------------------------------------------------------
@@ -325,6 +330,7 @@ __device__ void build_lists(const MoeFewArgs& a, ListScratch& B) {
 // The last block routes and lays out the slots; block t converts row t of x to f16, a warp per chunk.
 __global__ void __launch_bounds__(1024) moe_few_prepare_kernel(MoeFewArgs a) {
   __shared__ ListScratch scratch;
+  let_next_start();
   if ((int)blockIdx.x == a.T) {
     build_lists(a, scratch);
     return;
@@ -351,8 +357,8 @@ __global__ void __launch_bounds__(1024) moe_few_prepare_kernel(MoeFewArgs a) {
 //
 // Units are split evenly over the teams of S warps, in one contiguous run each (gate_up: slots outermost;
 // down: columns outermost, so that groups complete all along).  S is the least power of two that gives
-// every warp two units' worth of work, so that the last ones do not leave the card idle for long; a
-// team's warps take every S-th chunk and join in shared memory.
+// three quarters of the card's warps a unit, while a warp keeps two chunks; a team's warps take every S-th
+// chunk and join in shared memory.
 template <bool UP>
 __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -366,6 +372,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   const uint8_t* sfs = UP ? a.gu_sf : a.dn_sf;
   const float* s_gs = UP ? a.gu_sg : a.dn_sg;
 
+  if (UP) let_next_start();
+  wait_for_previous();
   uint32_t* slots = reinterpret_cast<uint32_t*>(smem + kRingBytes);
   uint8_t* token = reinterpret_cast<uint8_t*>(slots + P);
   const int n = a.lists[0];
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   const int units = n * groups;
   const int warps = gridDim.x * kWarps;
   int S = 1;
-  while (S < kWarps && 2 * S <= nch && units * S < 2 * warps) S *= 2;
+  while (S < kWarps && 4 * S <= nch && 4 * units * S < 3 * warps) S *= 2;
   const int team = (blockIdx.x * kWarps + warp) / S, teams = warps / S, part = warp & (S - 1);
   int u = (int)((int64_t)units * team / teams);
   const int u_end = (int)((int64_t)units * (team + 1) / teams);
@@ -616,9 +624,21 @@ cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   moe_few_prepare_kernel<<<a.T + 1, 1024, 0, st>>>(a);
-  moe_few_stream_kernel<true><<<num_sms, kWarps * 32, smem, st>>>(a);
-  moe_few_stream_kernel<false><<<num_sms, kWarps * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_sms);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, moe_few_stream_kernel<true>, a);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, moe_few_stream_kernel<false>, a);
 }
 
 }  // namespace nvfp4
