@@ -243,6 +243,16 @@ __device__ __forceinline__ float sort_lanes(float v) {
   }
   return v;
 }
+// The k-th largest of one value per lane: for a few, as many arg-max rounds; else the sorted list.
+__device__ __forceinline__ float kth_lane(float v, int k) {
+  if (k > 8) return __shfl_sync(0xffffffffu, sort_lanes(v), k - 1);
+  uint32_t o = order_bits(v), m = 0;
+  for (int r = 0; r < k; ++r) {
+    m = __reduce_max_sync(0xffffffffu, o);
+    if ((__ffs(__ballot_sync(0xffffffffu, o == m)) - 1) == (int)(threadIdx.x & 31)) o = 0;
+  }
+  return key_value((uint64_t)m << 32);
+}
 // Two descending lists -> their best 32, descending: the element-wise maximum of one and the other
 // reversed is bitonic and holds them; five exchanges sort it.
 __device__ __forceinline__ float merge_lanes(float a, float b) {
@@ -306,18 +316,22 @@ struct Span {
 //
 // Alternatives: every thread knows the largest of its logits; the k-th largest of these, tau, is a
 // lower bound of the k-th alternative, and only threads whose largest is not below it can hold one.
-// Their logits (k threads' worth unless logits tie) are read again and sorted in; a block's best k
-// then take their places by counting the larger ones.
+// Their logits (k threads' worth unless logits tie) are read again, those not below tau are listed, and
+// a listed one's place is the number of larger ones.  A list that would overflow (many ties at tau) is
+// replaced by one sorted list per warp.
 template <typename L, int W, bool TOP>
 __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobArgs a, int parts) {
   constexpr int N = Vec<L>::N;
   constexpr int kTeam = W * 32;
-  constexpr int U = 4;
   constexpr int kMaxParts = 8;
+  constexpr int kListed = 64;
+  constexpr int kCap = W > 1 ? 8 * kListed : kListed;
   __shared__ Stat part_stat[W > 1 ? W : 1];
   __shared__ float maxima[TOP && W > 1 ? W : 1][32];
-  __shared__ uint64_t cand[TOP && W > 1 ? W : 1][32];
-  __shared__ uint64_t best[32];
+  __shared__ uint64_t listed[TOP ? 8 : 1][kListed];  // per block (one list) or per warp (eight)
+  __shared__ int list_size[8];
+  __shared__ uint8_t holder[8][32];
+  __shared__ uint64_t best[TOP ? 8 : 1][32];         // the team's best k, in order
   // of the cluster's blocks, in the first one
   __shared__ Stat team_stat[kMaxParts];
   __shared__ uint64_t team_best[TOP && W > 1 ? kMaxParts * 32 : 1];
@@ -358,26 +372,33 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
 
   Stat st{-INFINITY, -INFINITY, 0.0f, 0.0f};
   int64_t v = sp.lo + tid;
-  for (; v + (U - 1) * kTeam < sp.hi; v += U * kTeam) {
-    uint4 r[U];
+  auto add_full = [&](auto& r) {
+    constexpr int n = sizeof(r) / sizeof(r[0]);
 #pragma unroll
-    for (int i = 0; i < U; ++i) r[i] = __ldg(sp.vec() + v + i * kTeam);
-    add_vectors<L, U>(st, r, c);
+    for (int i = 0; i < n; ++i) r[i] = __ldg(sp.vec() + v + i * kTeam);
+    add_vectors<L, n>(st, r, c);
+    v += n * kTeam;
+  };
+  // eight vectors on the way per thread (4096 x 131072 bf16: 162 us, four: 167 us; 1023 x 32000 f32: 24 us,
+  // 27 us); a warp's short row has no use for them
+  while (W > 1 && v + 7 * kTeam < sp.hi) {
+    uint4 r[8];
+    add_full(r);
   }
-  {
-    uint4 r[U - 1];
-    bool any = false;
+  while (v + 3 * kTeam < sp.hi) {
+    uint4 r[4];
+    add_full(r);
+  }
+  if (v < sp.hi) {
+    uint4 r[3];
 #pragma unroll
-    for (int i = 0; i < U - 1; ++i) {
+    for (int i = 0; i < 3; ++i) {
       // absent vectors: -inf, which adds nothing
       r[i] = sizeof(L) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
                             : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-      if (v + i * kTeam < sp.hi) {
-        r[i] = __ldg(sp.vec() + v + i * kTeam);
-        any = true;
-      }
+      if (v + i * kTeam < sp.hi) r[i] = __ldg(sp.vec() + v + i * kTeam);
     }
-    if (any) add_vectors<L, U - 1>(st, r, c);
+    add_vectors<L, 3>(st, r, c);
   }
   if (tid < sp.edge) add_element(st, Vec<L>::get(row + sp.edge_index(tid)), c);
   // the largest logit of this thread: where it is not above kLow, the maximum was taken all the same
@@ -385,13 +406,15 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
 
   join_lanes<32>(st);
   float tau = -INFINITY;
-  uint64_t mine = 0, thr = 0;
+  const int team_list = W > 1 ? 0 : warp;
   if (W > 1) {
     float sorted = 0.0f;
     if (lane == 0) part_stat[warp] = st;
     if (TOP) {
       sorted = sort_lanes(own_max);
       maxima[warp][lane] = sorted;
+      if (tid == 0) list_size[0] = 0;
+      if (tid < 32) best[0][tid] = 0;
     }
     __syncthreads();
     st = part_stat[lane & (W - 1)];
@@ -408,54 +431,90 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
       tau = maxima[0][k - 1];
     }
   } else if (TOP) {
-    tau = __shfl_sync(0xffffffffu, sort_lanes(own_max), k - 1);
-  }
-  if (TOP) {
-    thr = (uint64_t)order_bits(tau) << 32;  // below every logit that is not below tau
-    uint32_t holders = __ballot_sync(0xffffffffu, !(own_max < tau));
-    while (holders) {
-      const int src = __ffs(holders) - 1;
-      holders &= holders - 1;
-      const int64_t v0 = sp.lo + (W > 1 ? warp * 32 : 0) + src;
-      for (int64_t b = v0; b < sp.hi; b += 32 * kTeam) {  // a vector of that thread per lane
-        const int64_t w = b + (int64_t)lane * kTeam;
-        float x[N];
-        const bool has = w < sp.hi;
-        if (has) {
-          const uint4 r = __ldg(sp.vec() + w);
-          Vec<L>::unpack(r, x);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) offer(mine, thr, has ? x[i] : 0.0f, (uint32_t)(sp.head + w * N + i), has, k);
-      }
-    }
-    if (W == 1 || warp == 0) {
-      const bool has = lane < sp.edge;
-      const int64_t i = has ? sp.edge_index(lane) : 0;
-      offer(mine, thr, has ? Vec<L>::get(row + i) : 0.0f, (uint32_t)i, has, k);
-    }
-  }
-
-  if (TOP && W > 1) {
-    // a key's place is the number of larger ones; the block's best k, in order
-    cand[warp][lane] = lane < k ? mine : 0;
-    if (warp == 0) best[lane] = 0;
-    __syncthreads();
-    const uint64_t key = cand[warp][lane];
-    if (key != 0) {
-      int place = 0;
-      for (int i = 0; i < W; ++i)
-        for (int j = 0; j < k && cand[i][j] > key; ++j) ++place;
-      if (place < k) best[place] = key;
-    }
-    __syncthreads();
+    tau = kth_lane(own_max, k);
+    if (lane == 0) list_size[warp] = 0;
+    best[warp][lane] = 0;
   }
   uint64_t key = 0;
   int place = 32;
+  if (TOP) {
+    uint64_t* list = listed[team_list];
+    const uint64_t floor_key = (uint64_t)order_bits(tau) << 32;  // below every logit that is not below tau
+    auto put = [&](float x, uint32_t idx) {
+      const uint64_t q = order_key(x, idx);
+      if (q > floor_key) {
+        const int at = atomicAdd(&list_size[team_list], 1);
+        if (at < kCap) list[at] = q;
+      }
+    };
+    const uint32_t holders = __ballot_sync(0xffffffffu, !(own_max < tau));
+    if (!(own_max < tau)) holder[warp][__popc(holders & ((1u << lane) - 1u))] = (uint8_t)lane;
+    __syncwarp();
+    const int64_t per = (sp.hi - sp.lo + kTeam - 1) / kTeam;  // vectors of a thread
+    const int64_t todo = per * __popc(holders);
+    for (int64_t m = lane; m < todo; m += 32) {
+      const int h = (int)(m / per);
+      const int64_t w = sp.lo + (m - h * per) * kTeam + (W > 1 ? warp * 32 : 0) + holder[warp][h];
+      if (w < sp.hi) {
+        const uint4 r = __ldg(sp.vec() + w);
+        float x[N];
+        Vec<L>::unpack(r, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) put(x[i], (uint32_t)(sp.head + w * N + i));
+      }
+    }
+    if (tid < sp.edge) {
+      const int64_t i = sp.edge_index(tid);
+      put(Vec<L>::get(row + i), (uint32_t)i);
+    }
+    if (W > 1)
+      __syncthreads();
+    else
+      __syncwarp();
+    int size = list_size[team_list];
+    if (size > kCap) {
+      // too many: a sorted list of k per warp, of the warp's share of the row
+      uint64_t mine = 0, thr = 0;
+      for (int64_t b = sp.lo + (W > 1 ? warp * 32 : 0); b < sp.hi; b += kTeam) {
+        const int64_t w = b + lane;
+        const bool has = w < sp.hi;
+        float x[N];
+        Vec<L>::unpack(has ? __ldg(sp.vec() + w) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) offer(mine, thr, x[i], (uint32_t)(sp.head + w * N + i), has, k);
+      }
+      if (W == 1 || warp == 0) {
+        const bool has = lane < sp.edge;
+        const int64_t i = has ? sp.edge_index(lane) : 0;
+        offer(mine, thr, has ? Vec<L>::get(row + i) : 0.0f, (uint32_t)i, has, k);
+      }
+      if (W > 1) {
+        __syncthreads();
+        list[32 * warp + lane] = lane < k ? mine : 0;
+        __syncthreads();
+        size = 32 * W;
+      } else {
+        list[lane] = mine;
+        __syncwarp();
+        size = 32;
+      }
+    }
+    // the place of each listed logit among them (zeros are none)
+    for (int i = tid; i < size; i += kTeam) {
+      const uint64_t q = list[i];
+      int larger = 0;
+      for (int j = 0; j < size; ++j) larger += list[j] > q;
+      if (q != 0 && larger < k) best[team_list][larger] = q;
+    }
+    if (W > 1)
+      __syncthreads();
+    else
+      __syncwarp();
+  }
   if (W > 1 && parts > 1) {
     cluster_wait();  // every block of the cluster runs: the first one's shared memory may be written
     if (tid == 0) store_remote(&team_stat[part], st);
-    if (TOP && tid < 32) store_remote(&team_best[32 * part + tid], best[tid]);
+    if (TOP && tid < 32) store_remote(&team_best[32 * part + tid], best[0][tid]);
     __syncwarp();
     cluster_arrive();
     cluster_wait();
@@ -468,11 +527,11 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
       if (key != 0) {
         place = 0;
         for (int i = 0; i < parts; ++i)
-          for (int j = 0; j < k && team_best[32 * i + j] > key; ++j) ++place;
+          for (int j = 0; place < k && j < k && team_best[32 * i + j] > key; ++j) ++place;
       }
     }
   } else if (TOP && tid < 32) {
-    key = W > 1 ? best[tid] : mine;
+    key = best[team_list][tid];
     place = tid;
   }
 
@@ -515,7 +574,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
     if (a.entropy) a.entropy[t] = h;
     if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(bad ? NAN : st.m, st.M, ls, h);
   }
-  if (TOP && place < k && (key != 0 || place == tid)) {
+  if (TOP && place < k && key != 0) {
     a.top_ids[t * k + place] = key_index(key);
     a.top_lp[t * k + place] = !empty && !(st.s < INFINITY) ? NAN : log_prob(key_value(key));
   }
@@ -524,8 +583,10 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
 // dlogits = 2^y (A + B y) + [v = id] g_lp / temperature, with the row's factors A, B.  W > 1: a block
 // takes a stretch of a row, W = 1: a warp takes a row.  16-byte accesses where the row of the logits and
 // of the gradient have the same phase.
+// Eight blocks a SM keep enough bytes on the way for reads and writes together (4096 x 131072 bf16: 397 us
+// at four, 347 us at six, 334 us at eight, 6.4 TB/s).
 template <typename L, int W>
-__global__ void __launch_bounds__(256) logprobs_backward_kernel(LogprobBwdArgs a, int64_t stretches) {
+__global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(LogprobBwdArgs a, int64_t stretches) {
   constexpr int N = Vec<L>::N;
   constexpr int kTeam = W * 32;
   constexpr int U = 4;

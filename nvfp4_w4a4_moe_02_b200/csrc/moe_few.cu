@@ -22,6 +22,8 @@
 //   - The ring is filled by asynchronous copies, three steps ahead: a warp has six scoreboards for its
 //     loads, and a ring in registers waits for its youngest load with its oldest (measured: 3.6 TB/s
 //     without any arithmetic, at any depth).
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -614,17 +616,32 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
 
 size_t moe_few_list_words(int64_t T, int32_t k, int64_t H) { return (size_t)(list_arrived((int)(T * k)) + H / 64); }
 
+// Once per device and kernel: the most shared memory that a call can need.
+static cudaError_t allow_shared_memory() {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kMost = kRingBytes + kFewMaxPairs * 5;
+  static_assert(kMost <= 227 * 1024, "the most pairs fit");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
+  for (const void* f : {reinterpret_cast<const void*>(moe_few_stream_kernel<true>),
+                        reinterpret_cast<const void*>(moe_few_stream_kernel<false>)}) {
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+  }
+  done.fetch_or(bit);
+  return cudaSuccess;
+}
+
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st) {
   const int P = a.T * a.k;
   const int smem = kRingBytes + P * 4 + token_words(P) * 4;
-  static_assert(kRingBytes + kFewMaxPairs * 5 <= 227 * 1024, "the most pairs fit");
-  for (const void* f : {reinterpret_cast<const void*>(moe_few_stream_kernel<true>),
-                        reinterpret_cast<const void*>(moe_few_stream_kernel<false>)}) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_shared_memory();
+  if (e != cudaSuccess) return e;
   moe_few_prepare_kernel<<<a.T + 1, 1024, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

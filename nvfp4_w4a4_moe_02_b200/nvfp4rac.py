@@ -677,19 +677,24 @@ class _On:
     """Makes the tensors' device current and `stream` (None: that device's current stream) the one
     that buffers are allocated on and kernels are launched on."""
 
+    __slots__ = ("ctx", "index")
+
     def __init__(self, device: torch.device, stream=None):
-        self.ctx = None
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.index = device.index
         if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
             self.ctx = torch.cuda.stream(stream)
-        elif device.index is not None and device.index != torch.cuda.current_device():
+        elif self.index != torch.cuda.current_device():
             self.ctx = torch.cuda.device(device)
+        else:
+            self.ctx = None
 
     def __enter__(self) -> int:
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object costs as much as a launch
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -828,8 +833,9 @@ class _TokenLogprobsFn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_lp, g_ent, *_):
         logits, ids, stats = ctx.saved_tensors
-        g = [None if t is None else t.to(torch.float32).contiguous() for t in (g_lp, g_ent)]
-        return token_logprobs_backward(logits, ids, stats, ctx.temperature, *g), None, None, None, None, None
+        g_lp = None if g_lp is None else g_lp.contiguous()    # an expanded gradient has no rows of its own
+        g_ent = None if g_ent is None else g_ent.contiguous()
+        return token_logprobs_backward(logits, ids, stats, ctx.temperature, g_lp, g_ent), None, None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float = 1.0, top: int = 0,
