@@ -466,7 +466,7 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
                                           void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
-/* moe_w4a16_layer -- a whole MoE layer for a few tokens (T <= 64) in three kernels: routing,  */
+/* moe_w4a16_layer -- a whole MoE layer for a few tokens (T <= 64) in four kernels: routing,   */
 /* gate_up with SwiGLU, down and the weighted combine.  Activations stay bf16: at a few tokens */
 /* the layer is bound by the bytes of the touched experts' weights, so that nothing is gained  */
 /* by quantising them, no residual is needed (W_sel is not read), and the function is the      */

@@ -249,10 +249,10 @@ struct MoeFewArgs {
   uint16_t* h;                 // f16 [T k x I]: scaled SwiGLU outputs, rows in slot order
   float* h_scale;              // [T k x I / 32]
   float* y;                    // [T k x H]: outputs of the pairs, rows in slot order
-  int32_t* lists;              // moe_few_list_words(T, k, H) words
+  int32_t* lists;              // moe_few_list_words(T, k) words
   int32_t* status;
 };
-size_t moe_few_list_words(int64_t T, int32_t k, int64_t H);
+size_t moe_few_list_words(int64_t T, int32_t k);
 cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st);
 
 // ---- token log probabilities (csrc/logprobs.cu)

@@ -1,5 +1,5 @@
-// A whole mixture-of-experts layer for a few tokens: a small kernel that routes and lays the work out,
-// gate_up with SwiGLU, and down with the weighted combine.  Activations stay bf16 (the trainer's side of
+// A whole mixture-of-experts layer for a few tokens in four kernels: routing and layout, gate_up with
+// SwiGLU, down, and the weighted combine.  Activations stay bf16 (the trainer's side of
 // the method: weights fake-quantised, activations not), weights are the packed NVFP4 ones.
 //
 //   ids_t, w_t = the k largest logits of token t and their renormalised softmax
@@ -42,13 +42,12 @@ constexpr int kRedBytes = kTiles * 512;         // a warp's sums, for the warps 
 constexpr int kRingBytes = kWarps * (kWarpBytes + kRedBytes);
 
 // Workspace words: [0] slots n; a word per slot from kListHead on (expert, first pair << 10, count << 21);
-// token of each pair in slot order (bytes); place in slot order of pair t * k + j (-1: none); arrivals
-// per group of output columns.
+// token of each pair in slot order (bytes); place in slot order of pair t * k + j (-1: none).
 constexpr int kListHead = 16;
 __host__ __device__ inline int token_words(int P) { return (P + 3) / 4; }
 __host__ __device__ inline int list_tokens(int P) { return kListHead + P; }
 __host__ __device__ inline int list_places(int P) { return list_tokens(P) + token_words(P); }
-__host__ __device__ inline int list_arrived(int P) { return list_places(P) + P; }
+__host__ __device__ inline int list_words(int P) { return list_places(P) + P; }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -161,7 +160,7 @@ __device__ __forceinline__ void stretch_scale(int e, float* up, float* down) {
   *down = __uint_as_float((uint32_t)(e - 26) << 23);
 }
 
-// The three kernels of a call overlap their launches: a kernel lets the next one start at once, and
+// The kernels of a call overlap their launches: a kernel lets the next one start at once, and
 // that one waits here until this one's results are complete.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -170,7 +169,7 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // routing and layout
 // ----------------------------------------------------------------------------------------
 struct ListScratch {
-  uint16_t id[kFewMaxPairs];   // expert of pair t * k + j (0xFFFF: none)
+  alignas(16) uint16_t id[kFewMaxPairs];  // expert of pair t * k + j (0xFFFF: none)
   int cursor[kMaxRouteExperts];
 };
 
@@ -255,7 +254,6 @@ __device__ void build_lists(const MoeFewArgs& a, ListScratch& B) {
   uint32_t* slots = reinterpret_cast<uint32_t*>(a.lists + kListHead);
   uint8_t* token = reinterpret_cast<uint8_t*>(a.lists + list_tokens(P));
   int32_t* places = a.lists + list_places(P);
-  for (int i = threadIdx.x; i < a.H / 64; i += blockDim.x) a.lists[list_arrived(P) + i] = 0;
   if (P > 32)
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) B.cursor[e] = 0;
   for (int t = warp; t < a.T; t += blockDim.x / 32) route_token(a, t, B.id);
@@ -286,44 +284,46 @@ __device__ void build_lists(const MoeFewArgs& a, ListScratch& B) {
   for (int p = threadIdx.x; p < P; p += blockDim.x)
     if (B.id[p] != 0xFFFFu) atomicAdd(&B.cursor[B.id[p]], 1);
   __syncthreads();
-  if (warp != 0) return;
-  int n = 0, at = 0;  // slots and pairs before this group of experts
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int e = e0 + lane;
-    const int cnt = e < a.E ? B.cursor[e] : 0;
-    if (__ballot_sync(0xffffffffu, cnt > 0) == 0) continue;
-    int run = cnt | (cnt + kSlot - 1) / kSlot << 16;  // pairs low, slots high
-    const int own = run;
+  if (warp == 0) {
+    int n = 0, at = 0;  // slots and pairs before this group of experts
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int cnt = e < a.E ? B.cursor[e] : 0;
+      if (__ballot_sync(0xffffffffu, cnt > 0) == 0) continue;
+      int run = cnt | (cnt + kSlot - 1) / kSlot << 16;  // pairs low, slots high
+      const int own = run;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+      }
+      const int first = at + ((run - own) & 0xFFFF);
+      int i = n + ((run - own) >> 16);
+      for (int c = 0; c < cnt; c += kSlot, ++i) slots[i] = slot_word(e, first + c, min(kSlot, cnt - c));
+      if (cnt > 0) B.cursor[e] = first;
+      const int all = __shfl_sync(0xffffffffu, run, 31);
+      at += all & 0xFFFF;
+      n += all >> 16;
     }
-    const int first = at + ((run - own) & 0xFFFF);
-    int i = n + ((run - own) >> 16);
-    for (int c = 0; c < cnt; c += kSlot, ++i) slots[i] = slot_word(e, first + c, min(kSlot, cnt - c));
-    if (cnt > 0) B.cursor[e] = first;
-    const int all = __shfl_sync(0xffffffffu, run, 31);
-    at += all & 0xFFFF;
-    n += all >> 16;
+    if (lane == 0) a.lists[0] = n;
   }
-  if (lane == 0) a.lists[0] = n;
-  __syncwarp();
-  // ranks in pair order, 32 at a time
-  for (int p0 = 0; p0 < P; p0 += 32) {
-    const int p = p0 + lane;
-    const uint32_t e = p < P ? B.id[p] : 0xFFFFu;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    int base = 0;
-    if (e != 0xFFFFu) base = B.cursor[e];
-    __syncwarp();
+  __syncthreads();
+  // a pair's place: its expert's first, and the pairs of that expert before it (eight ids a read)
+  for (int p = threadIdx.x; p < P; p += blockDim.x) {
+    const uint32_t e = B.id[p], e2 = e | e << 16;
+    int place = -1;
     if (e != 0xFFFFu) {
-      token[base + before] = (uint8_t)(p / a.k);
-      if (before == 0) B.cursor[e] = base + __popc(same);
+      int twice = 0;
+      for (int q = 0; q < p >> 3; ++q) {
+        const uint4 v = reinterpret_cast<const uint4*>(B.id)[q];
+        twice += __popc(__vcmpeq2(v.x, e2)) + __popc(__vcmpeq2(v.y, e2)) + __popc(__vcmpeq2(v.z, e2)) +
+                 __popc(__vcmpeq2(v.w, e2));
+      }
+      place = B.cursor[e] + (twice >> 4);  // sixteen bits a match
+      for (int q = p & ~7; q < p; ++q) place += B.id[q] == e;
+      token[place] = (uint8_t)(p / a.k);
     }
-    if (p < P) places[p] = e != 0xFFFFu ? base + before : -1;
-    __syncwarp();
+    places[p] = place;
   }
 }
 
@@ -353,12 +353,9 @@ __global__ void __launch_bounds__(1024) moe_few_prepare_kernel(MoeFewArgs a) {
   }
 }
 
-// UP: gate_up + SwiGLU -> h.  Otherwise down: the products of each (slot, group of 64 output columns) go
-// to y in binary32, and the last warp to arrive at a group adds the pairs of every token in order of j:
-// the result does not depend on timing.
+// UP: gate_up + SwiGLU -> h.  Otherwise down: the products of each slot, in binary32, -> y.
 //
-// Units are split evenly over the teams of S warps, in one contiguous run each (gate_up: slots outermost;
-// down: columns outermost, so that groups complete all along).  S is the least power of two that gives
+// Units are split evenly over the teams of S warps, in one contiguous run each, slots outermost.  S is the least power of two that gives
 // three quarters of the card's warps a unit, while a warp keeps two chunks; a team's warps take every S-th
 // chunk and join in shared memory.
 template <bool UP>
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   const uint8_t* sfs = UP ? a.gu_sf : a.dn_sf;
   const float* s_gs = UP ? a.gu_sg : a.dn_sg;
 
-  if (UP) let_next_start();
+  let_next_start();
   wait_for_previous();
   uint32_t* slots = reinterpret_cast<uint32_t*>(smem + kRingBytes);
   uint8_t* token = reinterpret_cast<uint8_t*>(slots + P);
@@ -385,11 +382,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
       reinterpret_cast<uint32_t*>(token)[i] = (uint32_t)a.lists[list_tokens(P) + i];
   __syncthreads();
 
-  if (!UP && n == 0) {  // no token could be routed
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)a.T * a.H; i += (int64_t)gridDim.x * blockDim.x)
-      a.out[i / a.H * a.ldo + i % a.H] = 0;
-    return;
-  }
   const int units = n * groups;
   const int warps = gridDim.x * kWarps;
   int S = 1;
@@ -410,7 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   const uint8_t *pa = nullptr, *pas = nullptr;  // the lane's activations of chunk 0, their scales
   bool col = false;
   auto enter = [&](int unit) {
-    const int slot = UP ? unit / groups : unit % n, grp = UP ? unit % groups : unit / n;
+    const int slot = unit / groups, grp = unit % groups;
     const uint32_t w = slots[slot];
     const int64_t e = w & 1023u;
     const int first = (int)(w >> 10 & 2047u), cnt = (int)(w >> 21);
@@ -474,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   uint32_t step = 0, act = 0;
   float* red = reinterpret_cast<float*>(smem + kWarps * kWarpBytes);
   for (; u < u_end; ++u) {
-    const int slot = UP ? u / groups : u % n, grp = UP ? u % groups : u / n;
+    const int slot = u / groups, grp = u % groups;
     const uint32_t w = slots[slot];
     const int first = (int)(w >> 10 & 2047u), cnt = (int)(w >> 21);
     const float s_g = __ldg(s_gs + (w & 1023u)) * kSumUnit;
@@ -580,41 +572,42 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
           float* o = a.y + (int64_t)(first + 2 * t + j) * a.H + 128 * (grp >> 1) + 16 * (grp & 1) + g;
 #pragma unroll
           for (int r = 0; r < kTiles; ++r) {
-            __stcg(o + 32 * (r & 1) + 8 * (r >> 1), acc[r][j] * s_g);
-            __stcg(o + 64 + 32 * (r & 1) + 8 * (r >> 1), acc[r][2 + j] * s_g);
+            o[32 * (r & 1) + 8 * (r >> 1)] = acc[r][j] * s_g;
+            o[64 + 32 * (r & 1) + 8 * (r >> 1)] = acc[r][2 + j] * s_g;
           }
-        }
-      }
-      __threadfence();
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) last = atomicAdd(a.lists + list_arrived(P) + grp, 1) == n - 1;
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        __threadfence();
-        // the group's 64 columns: four stretches of 16, two columns a lane
-        const int c = 128 * (grp >> 1) + 16 * (grp & 1) + 32 * (lane >> 3) + 2 * (lane & 7);
-        const int32_t* place = a.lists + list_places(P);
-#pragma unroll 4
-        for (int tok = 0; tok < a.T; ++tok) {
-          float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-          for (int j = 0; j < a.k; ++j) {
-            const int p = place[tok * a.k + j];
-            if (p >= 0) {
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(a.y + (int64_t)p * a.H + c));
-              const float wt = a.topk_w[tok * a.k + j];
-              v.x = fmaf(wt, y.x, v.x);
-              v.y = fmaf(wt, y.y, v.y);
-            }
-          }
-          *reinterpret_cast<__nv_bfloat162*>(a.out + tok * a.ldo + c) = __floats2bfloat162_rn(v.x, v.y);
         }
       }
     }
   }
 }
 
-size_t moe_few_list_words(int64_t T, int32_t k, int64_t H) { return (size_t)(list_arrived((int)(T * k)) + H / 64); }
+// out[t] = sum_j w_tj y[place of (t, j)], j ascending; four columns a thread.
+__global__ void __launch_bounds__(128) moe_few_combine_kernel(MoeFewArgs a) {
+  const int64_t t = blockIdx.y;
+  const int c = 4 * (blockIdx.x * 128 + threadIdx.x);
+  wait_for_previous();
+  if (c >= a.H) return;
+  const int32_t* place = a.lists + list_places(a.T * a.k) + t * a.k;
+  const float* w = a.topk_w + t * a.k;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int j = 0; j < a.k; ++j) {
+    const int p = place[j];
+    if (p >= 0) {
+      const float4 y = *reinterpret_cast<const float4*>(a.y + (int64_t)p * a.H + c);
+      const float f = w[j];
+      v.x = fmaf(f, y.x, v.x);
+      v.y = fmaf(f, y.y, v.y);
+      v.z = fmaf(f, y.z, v.z);
+      v.w = fmaf(f, y.w, v.w);
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(a.out + t * a.ldo + c) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+size_t moe_few_list_words(int64_t T, int32_t k) { return (size_t)list_words((int)(T * k)); }
 
 // Once per device and kernel: the most shared memory that a call can need.
 static cudaError_t allow_shared_memory() {
@@ -655,7 +648,12 @@ cudaError_t launch_moe_few(const MoeFewArgs& a, int num_sms, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, moe_few_stream_kernel<true>, a);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, moe_few_stream_kernel<false>, a);
+  e = cudaLaunchKernelEx(&cfg, moe_few_stream_kernel<false>, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((a.H + 511) / 512), (unsigned)a.T);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, moe_few_combine_kernel, a);
 }
 
 }  // namespace nvfp4
