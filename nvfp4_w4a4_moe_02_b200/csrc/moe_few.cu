@@ -23,6 +23,7 @@
 //     loads, and a ring in registers waits for its youngest load with its oldest (measured: 3.6 TB/s
 //     without any arithmetic, at any depth).
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -147,6 +148,38 @@ __device__ __forceinline__ void mma_tile(float (&acc)[4], const uint4& klo, cons
   acc[1] = fmaf(part[1], d1, acc[1]);
   acc[2] = fmaf(part[2], d0, acc[2]);
   acc[3] = fmaf(part[3], d1, acc[3]);
+}
+
+// The same for one or two tokens, without scaling the codes: the lane's column holds token g % 2 for lanes
+// t = g / 2 of the quad and zero for the others, so that a lane's sums c0 .. c3 are those of its own 16
+// codes per row, one scale block, for either token, and take the block's scale as sums.  acc: the lane's
+// low row for the tokens 0, 1, then its high row, over its own codes only; d0, d1: the scales taken out of
+// the tokens' elements (first and second 16).  4 products on halves instead of 32.
+__device__ __forceinline__ void mma_tile_blocks(float (&acc)[4], const uint4& klo, const uint4& khi, uint32_t sf_lo,
+                                                uint32_t sf_hi, const uint32_t (&b)[16], float2 d0, float2 d1) {
+  const float2 sl = __half22float2(lane_scales(sf_lo)), sh = __half22float2(lane_scales(sf_hi));
+  const uint32_t lo[4] = {klo.x, klo.y, klo.z, klo.w}, hi[4] = {khi.x, khi.y, khi.z, khi.w};
+#pragma unroll
+  for (int blk = 0; blk < 2; ++blk) {
+    float part[4];
+#pragma unroll
+    for (int w = 2 * blk; w < 2 * blk + 2; ++w) {
+      const uint32_t a0 = decode_byte<0>(lo[w]), a1 = decode_byte<0>(hi[w]);
+      const uint32_t a2 = decode_byte<1>(lo[w]), a3 = decode_byte<1>(hi[w]);
+      if (w == 2 * blk)
+        mma16816_first(part, a0, a1, a2, a3, b[4 * w], b[4 * w + 1]);
+      else
+        mma16816(part, a0, a1, a2, a3, b[4 * w], b[4 * w + 1]);
+      mma16816(part, decode_byte<2>(lo[w]), decode_byte<2>(hi[w]), decode_byte<3>(lo[w]), decode_byte<3>(hi[w]),
+               b[4 * w + 2], b[4 * w + 3]);
+    }
+    const float l = blk ? sl.y : sl.x, h = blk ? sh.y : sh.x;
+    const float e0 = blk ? d0.y : d0.x, e1 = blk ? d1.y : d1.x;
+    acc[0] = fmaf(part[0], l * e0, acc[0]);
+    acc[1] = fmaf(part[1], l * e1, acc[1]);
+    acc[2] = fmaf(part[2], h * e0, acc[2]);
+    acc[3] = fmaf(part[3], h * e1, acc[3]);
+  }
 }
 
 // The power of two that brings a magnitude of binary32 exponent field e to [2^14, 2^15), and its
@@ -471,47 +504,86 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
     const int first = (int)(w >> 10 & 2047u), cnt = (int)(w >> 21);
     const float s_g = __ldg(s_gs + (w & 1023u)) * kSumUnit;
     float acc[kTiles][4] = {};
-    for (int i = 0; i < my_chunks; ++i) {
-      uint32_t b[16] = {};
-      float d0 = 0.0f, d1 = 0.0f;
+    auto stream = [&](auto few) {
+      for (int i = 0; i < my_chunks; ++i) {
+        uint32_t b[16] = {};
+        float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
 #pragma unroll
-      for (int pr = 0; pr < 2; ++pr) {
-        copies_wait<kSteps - 1>();
-        __syncwarp();  // the scales of a row are copied by one lane and read by two
-        const uint32_t src = base + step;
-        const uint4 lo0 = lds16(src + 16 * lane), lo1 = lds16(src + 16 * lane + 512);
-        const uint4 hi0 = lds16(src + 16 * lane + 1024), hi1 = lds16(src + 16 * lane + 1536);
-        const uint4 sf = lds16(src + 2048 + 32 * g + 16 * (t >> 1));
-        if (pr == 0) {
-          const bool in = UP || 128 * (part + S * i) + 32 * t < cols;
-          float2 f = make_float2(0.0f, 0.0f);
-          if (g < cnt && in) {
+        for (int pr = 0; pr < 2; ++pr) {
+          copies_wait<kSteps - 1>();
+          __syncwarp();  // the scales of a row are copied by one lane and read by two
+          const uint32_t src = base + step;
+          const uint4 lo0 = lds16(src + 16 * lane), lo1 = lds16(src + 16 * lane + 512);
+          const uint4 hi0 = lds16(src + 16 * lane + 1024), hi1 = lds16(src + 16 * lane + 1536);
+          const uint4 sf = lds16(src + 2048 + 32 * g + 16 * (t >> 1));
+          if (pr == 0) {
+            const bool in = UP || 128 * (part + S * i) + 32 * t < cols;
+            const uint32_t from = acts + act;
+            if constexpr (few.value) {
+              if (in) {
+                const int tok = g & 1;
+                if (t == g >> 1 && tok < cnt) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(acts + act + 512 * q + 16 * lane);
-            f = lds8(acts + act + 2048 + 8 * lane);
+                  for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(from + 512 * q + 16 * (4 * tok + t));
+                }
+                d0 = lds8(from + 2048 + 8 * t);
+                if (cnt > 1) d1 = lds8(from + 2048 + 32 + 8 * t);
+                if (UP) {  // one scale per chunk
+                  d0.y = d0.x;
+                  d1.y = d1.x;
+                }
+              }
+            } else {
+              float2 f = make_float2(0.0f, 0.0f);
+              if (g < cnt && in) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(from + 512 * q + 16 * lane);
+                f = lds8(from + 2048 + 8 * lane);
+              }
+              float d = f.x;
+              if (!UP) {
+                // one scale per column and chunk: the largest; the others' elements take the quotient (a
+                // power of two).  Of the lane's 32 elements the first and the second 16 have a scale each.
+                d = fmaxf(fmaxf(f.x, f.y), 1.17549435e-38f);
+                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
+                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2));
+                const float inv = __uint_as_float(0x7F000000u - __float_as_uint(d));
+                const uint32_t q0 = pack_f16(f.x * inv, f.x * inv), q1 = pack_f16(f.y * inv, f.y * inv);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) b[q] = hmul2(b[q], q < 8 ? q0 : q1);
+              }
+              d0.x = __shfl_sync(0xffffffffu, d, 8 * t);
+              d1.x = __shfl_sync(0xffffffffu, d, 8 * t + 4);
+            }
+            act ^= kActBytes;
           }
-          float d = f.x;
-          if (!UP) {
-            // one scale per column and chunk: the largest; the others' elements take the quotient (a power
-            // of two).  Of the lane's 32 elements the first and the second 16 have a scale each.
-            d = fmaxf(fmaxf(f.x, f.y), 1.17549435e-38f);
-            d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
-            d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2));
-            const float inv = __uint_as_float(0x7F000000u - __float_as_uint(d));
-            const uint32_t q0 = pack_f16(f.x * inv, f.x * inv), q1 = pack_f16(f.y * inv, f.y * inv);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) b[q] = hmul2(b[q], q < 8 ? q0 : q1);
+          if constexpr (few.value) {
+            mma_tile_blocks(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0, d1);
+            mma_tile_blocks(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0, d1);
+          } else {
+            mma_tile(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0.x, d1.x);
+            mma_tile(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0.x, d1.x);
           }
-          d0 = __shfl_sync(0xffffffffu, d, 8 * t);
-          d1 = __shfl_sync(0xffffffffu, d, 8 * t + 4);
-          act ^= kActBytes;
+          step = step == (kSteps - 1) * kStepBytes ? 0 : step + kStepBytes;
+          __syncwarp();  // every lane has read the place that is filled next
+          copy_step();
         }
-        mma_tile(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0, d1);
-        mma_tile(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0, d1);
-        step = step == (kSteps - 1) * kStepBytes ? 0 : step + kStepBytes;
-        __syncwarp();  // every lane has read the place that is filled next
-        copy_step();
       }
+    };
+    if (cnt <= 2) {
+      stream(std::true_type{});
+      // the quad's codes together, in the columns 0 and 1
+#pragma unroll
+      for (int r = 0; r < kTiles; ++r) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[r][q] += __shfl_xor_sync(0xffffffffu, acc[r][q], 1);
+          acc[r][q] += __shfl_xor_sync(0xffffffffu, acc[r][q], 2);
+        }
+      }
+    } else {
+      stream(std::false_type{});
     }
     if (S > 1) {
       float4* mine = reinterpret_cast<float4*>(red + warp * (kRedBytes / 4)) + lane;
