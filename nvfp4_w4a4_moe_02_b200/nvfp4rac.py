@@ -701,9 +701,13 @@ class _On:
             self.ctx.__exit__(*exc)
 
 
-def _arg(ok, text: str):
-    if not ok:
-        raise NVFP4Error(1, text)
+def _refuse(text: str):
+    raise NVFP4Error(1, text)
+
+
+def _check_like(t, shape, dtype, device, name: str):
+    if t is not None and not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == device):
+        _refuse(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
 
 
 def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Packed, w_down: Packed,
@@ -717,23 +721,26 @@ def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Pa
     trainer's function of fake-quantised weights.  `workspace` (uint8, moe_w4a16_workspace_size
     bytes) is allocated per call unless given; calls that may overlap need their own."""
     lib = load()
-    _arg(x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.stride(1) == 1,
-         "x must be a bf16 CUDA matrix with unit column stride")
+    if not (x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.stride(1) == 1):
+        _refuse("x must be a bf16 CUDA matrix with unit column stride")
     T, H = x.shape
     E, I = w_gate_up.slabs, w_down.cols
     dev = x.device
-    _arg(logits.shape == (T, E) and logits.dtype == torch.float32 and logits.is_contiguous() and logits.device == dev,
-         "logits must be contiguous float32 [T, E] on x's device")
-    _arg(w_gate_up.cols == H and w_down.slabs == E, "w_gate_up / w_down do not fit x and each other")
-    _arg(w_gate_up.codes.device == dev and w_down.codes.device == dev, "the weights must be on x's device")
-    for t, dtype, name in ((ids, torch.int32, "ids"), (w, torch.float32, "w")):
-        _arg(t is None or (t.shape == (T, k) and t.dtype == dtype and t.is_contiguous() and t.device == dev),
-             f"{name} must be a contiguous {dtype} [T, k] on x's device")
-    _arg(out is None or (out.shape == (T, H) and out.dtype == torch.bfloat16 and out.stride(1) == 1
-                         and out.device == dev), "out must be bf16 [T, H] with unit column stride on x's device")
-    _arg(workspace is None or (workspace.is_contiguous() and workspace.device == dev),
-         "workspace must be contiguous on x's device")
-    _arg(status is None or (status.dtype == torch.int32 and status.device == dev), "status must be int32 on x's device")
+    _check_like(logits, (T, E), torch.float32, dev, "logits")
+    if not (isinstance(k, int) and 0 < k <= E):
+        _refuse(f"k must be in [1, {E}]")
+    if w_gate_up.cols != H or w_down.slabs != E:
+        _refuse("w_gate_up / w_down do not fit x and each other")
+    if w_gate_up.codes.device != dev or w_down.codes.device != dev:
+        _refuse("the weights must be on x's device")
+    _check_like(ids, (T, k), torch.int32, dev, "ids")
+    _check_like(w, (T, k), torch.float32, dev, "w")
+    _check_like(status, (1,), torch.int32, dev, "status")
+    if out is not None and not (out.shape == (T, H) and out.dtype == torch.bfloat16 and out.stride(1) == 1
+                                and out.device == dev):
+        _refuse("out must be bf16 [T, H] with unit column stride on x's device")
+    if workspace is not None and not (workspace.is_contiguous() and workspace.device == dev):
+        _refuse("workspace must be contiguous on x's device")
     with _On(dev, stream) as s:
         ids = torch.empty(T, k, dtype=torch.int32, device=dev) if ids is None else ids
         w = torch.empty(T, k, dtype=torch.float32, device=dev) if w is None else w
@@ -755,32 +762,37 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: torch.Tensor | None    # float32 [T, top]
 
 
-def _logits_args(logits: torch.Tensor, ids: torch.Tensor, temperature: float):
-    _arg(logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16),
-         "logits must be a float32 or bf16 CUDA matrix")
+def _logits_args(logits: torch.Tensor, ids: torch.Tensor, temperature: float, status):
+    """The arguments that the forward and the backward call begin with."""
+    if not (logits.dim() == 2 and logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16)):
+        _refuse("logits must be a float32 or bf16 CUDA matrix")
     T, V = logits.shape
-    _arg(V == 1 or logits.stride(1) == 1, "logits must have unit column stride")
-    _arg(T <= 1 or logits.stride(0) >= V, "logits must have rows that do not overlap")
-    _arg(ids.shape == (T,) and ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous()
-         and ids.device == logits.device, "ids must be contiguous int32 or int64 [T] on the logits' device")
-    _arg(temperature > 0, "temperature must be positive")
-    dtype = OUT_F32 if logits.dtype == torch.float32 else OUT_BF16
-    return (logits.data_ptr(), dtype, T, V, logits.stride(0) if T > 1 else V, ids.data_ptr(), ids.element_size(),
-            1.0 / temperature)
+    ld, step = logits.stride()
+    if V > 1 and step != 1 or T > 1 and ld < V:
+        _refuse("logits must have unit column stride and rows that do not overlap")
+    if not (ids.shape == (T,) and ids.dtype in (torch.int64, torch.int32) and ids.is_contiguous()
+            and ids.device == logits.device):
+        _refuse("ids must be contiguous int32 or int64 [T] on the logits' device")
+    if not temperature > 0:
+        _refuse("temperature must be positive")
+    _check_like(status, (1,), torch.int32, logits.device, "status")
+    return (logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, T, V, ld if T > 1 else V,
+            ids.data_ptr(), ids.element_size(), 1.0 / temperature)
 
 
 def _logprobs_forward(logits, ids, temperature, top, status, stream, want_stats):
-    args = _logits_args(logits, ids, temperature)
+    args = _logits_args(logits, ids, temperature, status)
     T, V = logits.shape
+    if not (isinstance(top, int) and 0 <= top <= min(32, V)):
+        _refuse("top must be in [0, min(32, V)]")
     dev = logits.device
-    _arg(isinstance(top, int) and 0 <= top <= min(32, V), "top must be in [0, min(32, V)]")
-    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
-         "status must be int32 on the logits' device")
     with _On(dev, stream) as s:
         logprob, entropy = torch.empty(2, T, dtype=torch.float32, device=dev).unbind(0)
         stats = torch.empty(T, 4, dtype=torch.float32, device=dev) if want_stats else None
-        top_ids = torch.empty(T, top, dtype=torch.int32, device=dev) if top else None
-        top_lp = torch.empty(T, top, dtype=torch.float32, device=dev) if top else None
+        top_ids = top_lp = None
+        if top:
+            top_ids = torch.empty(T, top, dtype=torch.int32, device=dev)
+            top_lp = torch.empty(T, top, dtype=torch.float32, device=dev)
         _check(load().token_logprobs(*args, top, logprob.data_ptr(), entropy.data_ptr(), _ptr(stats), _ptr(top_ids),
                                      _ptr(top_lp), _ptr(status), s))
     return logprob, entropy, stats, top_ids, top_lp
@@ -792,19 +804,15 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torc
                             stream=None) -> torch.Tensor:
     """dL/dlogits from dL/dlogprob and dL/dentropy (float32 [T], None: zeros) and the `stats` of
     token_logprobs_forward; out may be the logits themselves."""
-    args = _logits_args(logits, ids, temperature)
+    args = _logits_args(logits, ids, temperature, status)
     T, V = logits.shape
     dev = logits.device
-    _arg(stats.shape == (T, 4) and stats.dtype == torch.float32 and stats.is_contiguous() and stats.device == dev,
-         "stats must be the forward call's float32 [T, 4]")
-    for g in (grad_logprob, grad_entropy):
-        _arg(g is None or (g.shape == (T,) and g.dtype == torch.float32 and g.is_contiguous() and g.device == dev),
-             "row gradients must be contiguous float32 [T] on the logits' device")
-    _arg(out is None or (out.shape == (T, V) and out.dtype == logits.dtype and (V == 1 or out.stride(1) == 1)
-                         and (T <= 1 or out.stride(0) >= V) and out.device == dev),
-         "out must be a matrix like the logits")
-    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
-         "status must be int32 on the logits' device")
+    _check_like(stats, (T, 4), torch.float32, dev, "stats")
+    _check_like(grad_logprob, (T,), torch.float32, dev, "grad_logprob")
+    _check_like(grad_entropy, (T,), torch.float32, dev, "grad_entropy")
+    if out is not None and not (out.shape == (T, V) and out.dtype == logits.dtype and (V == 1 or out.stride(1) == 1)
+                                and (T <= 1 or out.stride(0) >= V) and out.device == dev):
+        _refuse("out must be a matrix like the logits")
     with _On(dev, stream) as s:
         out = torch.empty(T, V, dtype=logits.dtype, device=dev) if out is None else out
         _check(load().token_logprobs_backward(*args, stats.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
@@ -821,8 +829,8 @@ def token_logprobs_forward(logits: torch.Tensor, ids: torch.Tensor, temperature:
 
 class _TokenLogprobsFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, ids, temperature, top, status, stream):
-        lp, ent, stats, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, True)
+    def forward(ctx, logits, ids, temperature, top, status):
+        lp, ent, stats, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, None, True)
         ctx.save_for_backward(logits, ids, stats)
         ctx.temperature = temperature
         ctx.set_materialize_grads(False)
@@ -835,7 +843,7 @@ class _TokenLogprobsFn(torch.autograd.Function):
         logits, ids, stats = ctx.saved_tensors
         g_lp = None if g_lp is None else g_lp.contiguous()    # an expanded gradient has no rows of its own
         g_ent = None if g_ent is None else g_ent.contiguous()
-        return token_logprobs_backward(logits, ids, stats, ctx.temperature, g_lp, g_ent), None, None, None, None, None
+        return token_logprobs_backward(logits, ids, stats, ctx.temperature, g_lp, g_ent), None, None, None, None
 
 
 def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float = 1.0, top: int = 0,
@@ -845,9 +853,12 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float =
 
     logits: float32 or bf16 [T, V], any row pitch; -inf is a masked token.  ids: int32 or int64;
     a negative id marks a padding row (zeros, top_ids -1, no gradient).  logprob and entropy carry
-    gradients to the logits."""
+    gradients to the logits; with them, another stream is chosen by making it current, so that the
+    backward pass follows."""
     if logits.requires_grad and torch.is_grad_enabled():
-        return TokenLogprobs(*_TokenLogprobsFn.apply(logits, ids, temperature, top, status, stream))
+        if stream is not None:
+            _refuse("with gradients, make the stream current instead of passing it")
+        return TokenLogprobs(*_TokenLogprobsFn.apply(logits, ids, temperature, top, status))
     lp, ent, _, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, False)
     return TokenLogprobs(lp, ent, ti, tl)
 

@@ -334,6 +334,55 @@ def test_captured_forward_and_backward(dev):
         assert all(torch.equal(x, y) for x, y in zip(out, ref))
 
 
+def test_captured_autograd(dev):
+    logits, ids = make(dev, 6, 3001, torch.float32, seed=12)
+    g = torch.randn(6, device=dev)
+
+    def step(x):
+        leaf = x.detach().requires_grad_()
+        r = R.token_logprobs(leaf, ids, temperature=0.9)
+        return torch.autograd.grad([r.logprob, r.entropy], [leaf], [g, g])[0]
+
+    want = step(logits)
+    x = logits.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_gradients_follow_the_current_stream(dev):
+    logits, ids = make(dev, 6, 3001, torch.float32, seed=13)
+    leaf = logits.clone().requires_grad_()
+    with pytest.raises(R.NVFP4Error):
+        R.token_logprobs(leaf, ids, stream=torch.cuda.Stream())
+    R.token_logprobs(leaf, ids).logprob.sum().backward()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = logits.clone().requires_grad_()
+        R.token_logprobs(other, ids).logprob.sum().backward()
+    torch.cuda.synchronize()
+    assert torch.equal(other.grad, leaf.grad)
+
+
+def test_no_second_derivative(dev):
+    logits, ids = make(dev, 2, 50, torch.float32)
+    leaf = logits.clone().requires_grad_()
+    (g,) = torch.autograd.grad(R.token_logprobs(leaf, ids).logprob.sum(), leaf, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_offsets_past_32_bits(dev):
     # the last rows start past 2^32 elements
     T, V = 70, 1 << 26

@@ -48,8 +48,8 @@ def values(p, e, dev):
     return torch.from_numpy(v).to(dev) * sf.double().repeat_interleave(16, 1).to(dev) * s.s_g.double()
 
 
-def reference(x, ids, w, pgu, pdn):
-    """(out, bound) in float64 for the given routing."""
+def reference(x, ids, w, pgu, pdn, weight_err=0.0):
+    """(out, bound) in float64 for the given routing; the bound allows for a relative error of the weights."""
     dev = x.device
     T, H = x.shape
     I = pdn.cols
@@ -58,7 +58,7 @@ def reference(x, ids, w, pgu, pdn):
     tol = torch.zeros_like(out)
     n = torch.arange(2 * I, device=dev)
     gate, up = n[n % 128 < 64], n[n % 128 >= 64]
-    gam = lambda K: (K + 32) * 2.0 ** -23
+    gam = lambda K: (K + 32) * 2.0 ** -23 + weight_err
     for e in torch.unique(ids[ids >= 0]).tolist():
         t, j = (ids == e).nonzero(as_tuple=True)
         W, D = values(pgu, e, dev), values(pdn, e, dev)
