@@ -6,7 +6,8 @@ memory and the current stream.  If the compiled library is missing, loading it r
 is no fallback implementation.
 
 Call names match the C ABI: ``nvfp4_quantize``, ``rac_calibrate``, ``pack_weights``,
-``w4a4_rac_gemm``, ``grouped_w4a4_rac_moe``, ``weight_qdq``.
+``w4a4_rac_gemm``, ``grouped_w4a4_rac_moe``, ``weight_qdq``, ``moe_w4a16_layer``,
+``token_logprobs``.
 """
 from __future__ import annotations
 
@@ -787,7 +788,8 @@ def _logprobs_forward(logits, ids, temperature, top, status, stream, want_stats)
         _refuse("top must be in [0, min(32, V)]")
     dev = logits.device
     with _On(dev, stream) as s:
-        logprob, entropy = torch.empty(2, T, dtype=torch.float32, device=dev).unbind(0)
+        logprob = torch.empty(T, dtype=torch.float32, device=dev)
+        entropy = torch.empty(T, dtype=torch.float32, device=dev)
         stats = torch.empty(T, 4, dtype=torch.float32, device=dev) if want_stats else None
         top_ids = top_lp = None
         if top:
