@@ -24,7 +24,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // -2^100, a bf16: for c in [2^-26, 2^27] kLow c is finite, and 2^(kLow c - M) is 0 for every M above it
 constexpr float kLow = -1.2676506002282294e30f;
-constexpr uint32_t kLowBf16x2 = 0xF180F180u;
 // A row that the fast form cannot hold: nothing above kLow, or |M| so large that its rounding (y at the
 // maximum, up to 2^-25 |M|) would no longer be a small power of two
 __device__ __forceinline__ bool needs_exact(float m, float M) { return !(m > kLow && fabsf(M) < 268435456.0f); }
@@ -46,14 +45,16 @@ struct Vec<float> {
     x[2] = __uint_as_float(r.z);
     x[3] = __uint_as_float(r.w);
   }
-  // x_i = max(l_i, kLow), NaN kept; returns the largest l, NaN skipped
-  static __device__ __forceinline__ float clamp(uint4& r) {
+  // A lower bound as clamp() takes it, not above `low`
+  static __device__ __forceinline__ uint32_t bound(float low) { return __float_as_uint(low); }
+  // x_i = max(l_i, low), NaN kept; returns the largest l, NaN skipped
+  static __device__ __forceinline__ float clamp(uint4& r, uint32_t low) {
     uint32_t* w = &r.x;
     const float m = fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float v;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(__uint_as_float(w[i])), "f"(kLow));
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(__uint_as_float(w[i])), "f"(__uint_as_float(low)));
       w[i] = __float_as_uint(v);
     }
     return m;
@@ -80,11 +81,15 @@ struct Vec<uint16_t> {  // bf16 bit patterns
     asm("max.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(a), "r"(b));
     return v;
   }
-  static __device__ __forceinline__ float clamp(uint4& r) {
+  static __device__ __forceinline__ uint32_t bound(float low) {
+    const __nv_bfloat16 b = __float2bfloat16_rd(low);
+    return (uint32_t)*reinterpret_cast<const uint16_t*>(&b) * 0x10001u;
+  }
+  static __device__ __forceinline__ float clamp(uint4& r, uint32_t low) {
     const uint32_t m = max2(max2(r.x, r.y), max2(r.z, r.w));
     uint32_t* w = &r.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(kLowBf16x2));
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(low));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
   static __device__ __forceinline__ float get(const uint16_t* p) { return bf16_bits_to_f32(*p); }
@@ -115,9 +120,15 @@ struct __align__(16) Stat {
 __device__ __forceinline__ void rebase(Stat& a, float M) {
   const float d = a.M - M;
   const float f = ex2(d);
-  // a part 2^-126 below adds nothing, and one without elements has d = -inf; NaN stays NaN
-  a.u = f == 0.0f ? 0.0f * a.s : f * fmaf(d, a.s, a.u);
-  a.s *= f;
+  if (f == 0.0f) {
+    // a part 2^-126 below adds nothing; its sums may even be infinite (a thread that saw only a mask's
+    // -1e15 has an M whose rounding is large), but NaN stays NaN
+    if (a.s == a.s) a.s = 0.0f;
+    a.u = a.s;
+  } else {
+    a.u = f * fmaf(d, a.s, a.u);
+    a.s *= f;
+  }
   a.M = M;
 }
 
@@ -143,9 +154,10 @@ __device__ __forceinline__ void join_lanes(Stat& a) {
 template <typename L, int U>
 __device__ __forceinline__ void add_vectors(Stat& a, uint4 (&r)[U], float c) {
   constexpr int N = Vec<L>::N;
-  float bm = Vec<L>::clamp(r[0]);
+  const uint32_t low = Vec<L>::bound(kLow);
+  float bm = Vec<L>::clamp(r[0], low);
 #pragma unroll
-  for (int i = 1; i < U; ++i) bm = fmaxf(bm, Vec<L>::clamp(r[i]));
+  for (int i = 1; i < U; ++i) bm = fmaxf(bm, Vec<L>::clamp(r[i], low));
   if (!(bm <= a.m)) {
     a.m = fmaxf(a.m, bm);
     if (a.m > kLow) rebase(a, a.m * c);
@@ -613,6 +625,9 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   }
   const float rs = ex2(-st.z);
   const float A = -rs * fmaf(gb, fmaf(st.z, -kLn2, st.w), ga), B = -rs * gb * kLn2;
+  // logits whose 2^y is 0 many times over count as this: A + B y stays finite
+  const float floor_l = (st.y - 16384.0f) / c;
+  const uint32_t low = Vec<L>::bound(floor_l);
   auto element = [&](float l, int64_t v) {
     if (zero) return 0.0f;
     float g;
@@ -620,7 +635,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
       const float q = fmaxf((l - st.x) * c - st.z, -1000.0f);  // log2 p
       g = -ex2(q) * fmaf(gb, fmaf(q, kLn2, st.w), ga) + (st.x - st.x);
     } else {
-      const float y = fmaf(l > kLow ? l : l != l ? l : kLow, c, -st.y);
+      const float y = fmaf(l < floor_l ? floor_l : l, c, -st.y);
       g = ex2(y) * fmaf(B, y, A);
     }
     return v == id ? g + ga : g;
@@ -654,7 +669,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = element(x[j], e0 + j);
       } else {
-        Vec<L>::clamp(r[i]);
+        Vec<L>::clamp(r[i], low);
         Vec<L>::unpack(r[i], x);
 #pragma unroll
         for (int j = 0; j < N; j += 2) {

@@ -187,6 +187,28 @@ def test_masks_and_padding(dev, V, dtype):
     assert got.logprob[1] == NINF and got.entropy[1] == 0 and (grad[1] == 0).all()
 
 
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e10, -1e15, -1e20, -1e30, -2e30, -1e38])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,temperature", [(700, 1.0), (5000, 0.5), (40000, 1e-6), (5000, 1e6)])
+def test_masks_by_large_negative_values(dev, V, temperature, dtype, mask):
+    # some threads see nothing but the mask's value, others nothing of it
+    logits, ids = make(dev, 5, V, dtype, seed=V)
+    logits *= temperature
+    logits[0, V // 3:] = mask
+    logits[1, 1:] = mask
+    logits[2, ::2] = mask
+    logits[3, :] = mask
+    logits[4, : V - 1] = mask
+    ids[1] = 0
+    ids[4] = V - 1
+    st = R.new_status(dev)
+    got, stats = R.token_logprobs_forward(logits, ids, temperature, 3, status=st)
+    R.check_status(st)
+    check_forward(logits, ids, temperature, got, 3)
+    g, h = torch.randn(5, device=dev), torch.randn(5, device=dev)
+    check_backward(logits, ids, temperature, g, h, R.token_logprobs_backward(logits, ids, stats, temperature, g, h))
+
+
 @pytest.mark.parametrize("V", [100, 5000])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_not_finite_rows(dev, V, dtype):
@@ -223,8 +245,8 @@ def test_ids_past_the_vocabulary(dev):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("order", ["ascending", "descending", "equal", "few values"])
-def test_top_alternatives_of_ordered_rows(dev, order, dtype):
-    V = 20000
+@pytest.mark.parametrize("V", [900, 20000, 140001])
+def test_top_alternatives_of_ordered_rows(dev, V, order, dtype):
     v = torch.linspace(-4, 4, V, device=dev).to(dtype)
     if order == "descending":
         v = v.flip(0)
