@@ -306,18 +306,18 @@ __device__ __forceinline__ void store_remote(uint64_t* p, uint64_t v) {
 template <typename L>
 struct Span {
   const L* row;
-  int64_t lo, hi;    // this share's vectors
-  int64_t head, V;
+  int lo, hi;        // this share's vectors
+  int head, V;
   int edge;          // elements that go one by one here
-  __device__ __forceinline__ Span(const L* r, int64_t v, int part, int parts) : row(r), V(v) {
+  __device__ __forceinline__ Span(const L* r, int v, int part, int parts) : row(r), V(v) {
     constexpr int N = Vec<L>::N;
-    head = min(v, (int64_t)((16 - (reinterpret_cast<uintptr_t>(r) & 15)) & 15) / (int64_t)sizeof(L));
-    const int64_t nvec = (v - head) / N;
-    lo = nvec * part / parts;
-    hi = nvec * (part + 1) / parts;
-    edge = part == 0 ? (int)(v - nvec * N) : 0;
+    head = min(v, (int)((16 - (reinterpret_cast<uintptr_t>(r) & 15)) & 15) / (int)sizeof(L));
+    const int nvec = (v - head) / N;
+    lo = (int)((int64_t)nvec * part / parts);
+    hi = (int)((int64_t)nvec * (part + 1) / parts);
+    edge = part == 0 ? v - nvec * N : 0;
   }
-  __device__ __forceinline__ int64_t edge_index(int i) const { return i < head ? i : V - edge + i; }
+  __device__ __forceinline__ int edge_index(int i) const { return i < head ? i : V - edge + i; }
   __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(row + head); }
 };
 
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
   }
   const float c = a.inv_temp * kLog2e;
   const L* row = reinterpret_cast<const L*>(a.logits) + t * a.ld;
-  const Span<L> sp(row, a.V, part, parts);
+  const Span<L> sp(row, (int)a.V, part, parts);
   if (W > 1 && parts > 1) {
     __syncwarp();
     cluster_arrive();
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
   if (first) l_id = Vec<L>::get(row + id);
 
   Stat st{-INFINITY, -INFINITY, 0.0f, 0.0f};
-  int64_t v = sp.lo + tid;
+  int v = sp.lo + tid;
   auto add_full = [&](auto& r) {
     constexpr int n = sizeof(r) / sizeof(r[0]);
 #pragma unroll
@@ -462,11 +462,12 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
     const uint32_t holders = __ballot_sync(0xffffffffu, !(own_max < tau));
     if (!(own_max < tau)) holder[warp][__popc(holders & ((1u << lane) - 1u))] = (uint8_t)lane;
     __syncwarp();
-    const int64_t per = (sp.hi - sp.lo + kTeam - 1) / kTeam;  // vectors of a thread
-    const int64_t todo = per * __popc(holders);
-    for (int64_t m = lane; m < todo; m += 32) {
-      const int h = (int)(m / per);
-      const int64_t w = sp.lo + (m - h * per) * kTeam + (W > 1 ? warp * 32 : 0) + holder[warp][h];
+    const int per = (sp.hi - sp.lo + kTeam - 1) / kTeam;  // vectors of a thread
+    const int todo = per * __popc(holders);
+    const volatile int* listed_now = &list_size[team_list];
+    for (int m = lane; m < todo && *listed_now <= kCap; m += 32) {
+      const int h = m / per;
+      const int w = sp.lo + (m - h * per) * kTeam + (W > 1 ? warp * 32 : 0) + holder[warp][h];
       if (w < sp.hi) {
         const uint4 r = __ldg(sp.vec() + w);
         float x[N];
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
       }
     }
     if (tid < sp.edge) {
-      const int64_t i = sp.edge_index(tid);
+      const int i = sp.edge_index(tid);
       put(Vec<L>::get(row + i), (uint32_t)i);
     }
     if (W > 1)
@@ -487,8 +488,8 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
     if (size > kCap) {
       // too many: a sorted list of k per warp, of the warp's share of the row
       uint64_t mine = 0, thr = 0;
-      for (int64_t b = sp.lo + (W > 1 ? warp * 32 : 0); b < sp.hi; b += kTeam) {
-        const int64_t w = b + lane;
+      for (int b = sp.lo + (W > 1 ? warp * 32 : 0); b < sp.hi; b += kTeam) {
+        const int w = b + lane;
         const bool has = w < sp.hi;
         float x[N];
         Vec<L>::unpack(has ? __ldg(sp.vec() + w) : make_uint4(0, 0, 0, 0), x);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
       }
       if (W == 1 || warp == 0) {
         const bool has = lane < sp.edge;
-        const int64_t i = has ? sp.edge_index(lane) : 0;
+        const int i = has ? sp.edge_index(lane) : 0;
         offer(mine, thr, has ? Vec<L>::get(row + i) : 0.0f, (uint32_t)i, has, k);
       }
       if (W > 1) {
@@ -628,7 +629,8 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   // logits whose 2^y is 0 many times over count as this: A + B y stays finite
   const float floor_l = (st.y - 16384.0f) / c;
   const uint32_t low = Vec<L>::bound(floor_l);
-  auto element = [&](float l, int64_t v) {
+  const int at_id = (int)id;
+  auto element = [&](float l, int v) {
     if (zero) return 0.0f;
     float g;
     if (exact) {
@@ -638,28 +640,27 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
       const float y = fmaf(l < floor_l ? floor_l : l, c, -st.y);
       g = ex2(y) * fmaf(B, y, A);
     }
-    return v == id ? g + ga : g;
+    return v == at_id ? g + ga : g;
   };
-  const Span<L> sp(row, a.V, 0, 1);
+  const Span<L> sp(row, (int)a.V, 0, 1);
   if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grow)) & 15) != 0) {
-    const int64_t per = (a.V + stretches - 1) / stretches;
-    const int64_t end = min(a.V, (at + 1) * per);
-    for (int64_t v = at * per + tid; v < end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
+    const int end = (int)(a.V * (at + 1) / stretches);
+    for (int v = (int)(a.V * at / stretches) + tid; v < end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
     return;
   }
   uint4* gvec = reinterpret_cast<uint4*>(grow + sp.head);
-  const int64_t lo = sp.hi * at / stretches, hi = sp.hi * (at + 1) / stretches;
+  const int lo = (int)(sp.hi * at / stretches), hi = (int)(sp.hi * (at + 1) / stretches);
   const float2 c2 = make_float2(c, c), M2 = make_float2(-st.y, -st.y);
   const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
-  for (int64_t v0 = lo + tid; v0 < hi; v0 += U * kTeam) {
+  for (int v0 = lo + tid; v0 < hi; v0 += U * kTeam) {
     uint4 r[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) r[i] = v0 + i * kTeam < hi && !zero ? sp.vec()[v0 + i * kTeam] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t v = v0 + i * kTeam;
+      const int v = v0 + i * kTeam;
       if (v >= hi) break;
-      const int64_t e0 = sp.head + v * N;
+      const int e0 = sp.head + v * N;
       float x[N];
       if (zero) {
 #pragma unroll
@@ -678,17 +679,17 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
           x[j] = g.x;
           x[j + 1] = g.y;
         }
-        if (id >= e0 && id < e0 + N) {
+        if ((uint32_t)(at_id - e0) < (uint32_t)N) {
 #pragma unroll
           for (int j = 0; j < N; ++j)
-            if (e0 + j == id) x[j] += ga;
+            if (e0 + j == at_id) x[j] += ga;
         }
       }
       gvec[v] = Vec<L>::pack(x);
     }
   }
   if (at == 0 && tid < sp.edge) {
-    const int64_t v = sp.edge_index(tid);
+    const int v = sp.edge_index(tid);
     Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
   }
 }

@@ -423,6 +423,24 @@ def test_offsets_past_32_bits(dev):
     assert (grad[T - 2] == 0).all()
 
 
+def test_the_longest_row(dev):
+    # V = 2^31 - 1: uniform but for the last token, e^5 times as likely; every sum below is exact or closed
+    V = (1 << 31) - 1
+    logits = torch.zeros(1, V, dtype=torch.bfloat16, device=dev)
+    logits[0, V - 1] = 5.0
+    ids = torch.tensor([V - 1], device=dev)
+    got, stats = R.token_logprobs_forward(logits, ids, 1.0, 3)
+    lse = math.log(V - 1 + math.exp(5.0))
+    assert got.top_ids.tolist() == [[V - 1, 0, 1]]
+    # sums of 2^20 equal terms per thread; lse is near 21.5, a step of binary32 there is 2^-19
+    assert abs(got.logprob.item() - (5.0 - lse)) <= 1e-5
+    assert abs(got.entropy.item() - (lse - 5.0 * math.exp(5.0 - lse))) <= 1e-5
+    grad = R.token_logprobs_backward(logits, ids, stats, 1.0, torch.ones(1, device=dev), out=logits)
+    assert abs(grad[0, V - 1].item() - (1.0 - math.exp(5.0 - lse))) <= 2.0 ** -8
+    for v in (0, 1, V // 2, V - 2):
+        assert abs(grad[0, v].item() / -math.exp(-lse) - 1.0) <= 2.0 ** -7
+
+
 def test_refusals(dev):
     logits, ids = make(dev, 4, 64, torch.float32)
     st = torch.zeros(4, 4, device=dev)
