@@ -108,7 +108,8 @@ struct Vec<uint16_t> {  // bf16 bit patterns
   }
 };
 
-constexpr int64_t kWarpRow = 1024;  // rows up to this length go to a warp each
+constexpr int64_t kWarpRow = 1024;   // rows up to this length go to a warp each
+constexpr int64_t kPairRow = 32768;  // and up to this one to two, where there are many
 
 // Running statistics of a part of a row against the reference M = RN(m c), m the largest logit seen.
 // Nothing above kLow yet: m is what it is, M = -inf, s = u = 0.  A NaN or +inf ends as s = NaN.
@@ -323,8 +324,9 @@ struct Span {
 
 }  // namespace
 
-// One row per team.  W > 1: a team is a cluster of `parts` blocks of W warps, each with its share of
-// the row, joined through the cluster's shared memory; W = 1: a block holds eight one-warp teams.
+// One row per team.  W = 8: a team is a cluster of `parts` blocks, each with its share of the row, joined
+// through the cluster's shared memory; W = 2: a block of two warps; W = 1: a block holds eight one-warp
+// teams.
 //
 // Alternatives: every thread knows the largest of its logits; the k-th largest of these, tau, is a
 // lower bound of the k-th alternative, and only threads whose largest is not below it can hold one.
@@ -336,17 +338,16 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
   constexpr int N = Vec<L>::N;
   constexpr int kTeam = W * 32;
   constexpr int kMaxParts = 8;
-  constexpr int kListed = 64;
-  constexpr int kCap = W > 1 ? 8 * kListed : kListed;
+  constexpr int kCap = W == 1 ? 128 : W == 2 ? 256 : 512;
   __shared__ Stat part_stat[W > 1 ? W : 1];
   __shared__ float maxima[TOP && W > 1 ? W : 1][32];
-  __shared__ uint64_t listed[TOP ? 8 : 1][kListed];  // per block (one list) or per warp (eight)
+  __shared__ uint64_t listed[W > 1 ? 1 : 8][TOP ? kCap : 1];  // per block, or per warp
   __shared__ int list_size[8];
   __shared__ uint8_t holder[8][32];
-  __shared__ uint64_t best[TOP ? 8 : 1][32];         // the team's best k, in order
+  __shared__ uint64_t best[TOP && W == 1 ? 8 : 1][32];         // the team's best k, in order
   // of the cluster's blocks, in the first one
   __shared__ Stat team_stat[kMaxParts];
-  __shared__ uint64_t team_best[TOP && W > 1 ? kMaxParts * 32 : 1];
+  __shared__ uint64_t team_best[TOP && W == 8 ? kMaxParts * 32 : 1];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int tid = W > 1 ? threadIdx.x : lane;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
   const float c = a.inv_temp * kLog2e;
   const L* row = reinterpret_cast<const L*>(a.logits) + t * a.ld;
   const Span<L> sp(row, (int)a.V, part, parts);
-  if (W > 1 && parts > 1) {
+  if (W == 8 && parts > 1) {
     __syncwarp();
     cluster_arrive();
   }
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
     else
       __syncwarp();
   }
-  if (W > 1 && parts > 1) {
+  if (W == 8 && parts > 1) {
     cluster_wait();  // every block of the cluster runs: the first one's shared memory may be written
     if (tid == 0) store_remote(&team_stat[part], st);
     if (TOP && tid < 32) store_remote(&team_best[32 * part + tid], best[0][tid]);
@@ -708,6 +709,13 @@ template <typename L, bool TOP>
 cudaError_t launch_forward(const LogprobArgs& a, int num_sms, cudaStream_t st) {
   if (a.V <= kWarpRow) {
     logprobs_kernel<L, 1, TOP><<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>(a, 1);
+    return cudaGetLastError();
+  }
+  // Eight warps that meet for a short row wait for one another (us, two warps against eight: 2000 x 2000
+  // bf16 5.1, 11.1; 4000 x 8000 19.6, 29.6; 2000 x 32000 27.7, 28.7); rows that do not fill the card with
+  // eight each are done sooner so (20 x 8000 f32 5.0, 3.8; 300 x 16000 6.9, 5.4)
+  if (a.V <= kPairRow && a.T >= 4 * (int64_t)num_sms) {
+    logprobs_kernel<L, 2, TOP><<<(unsigned)a.T, 64, 0, st>>>(a, 1);
     return cudaGetLastError();
   }
   const int parts = row_parts(a.T, a.V, num_sms);

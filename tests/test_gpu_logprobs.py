@@ -106,7 +106,8 @@ def make(dev, T, V, dtype, pitch=None, off=0, seed=0, scale=3.0):
 
 SHAPES = [(1, 1, 1), (3, 2, 2), (2, 7, 7), (5, 31, 5), (9, 128, 32), (33, 515, 4), (16, 1000, 0), (4, 1024, 1),
           (4, 1025, 20), (6, 2049, 8), (300, 333, 3), (3, 8191, 32), (3, 32000, 0), (5, 50257, 8), (1, 131072, 20),
-          (40, 131073, 5), (2, 300001, 32), (150, 20011, 0), (320, 9000, 2), (700, 4100, 0)]
+          (40, 131073, 5), (2, 300001, 32), (150, 20011, 0), (320, 9000, 2), (700, 4100, 0), (700, 1025, 32),
+          (601, 32768, 3), (1300, 1777, 8)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -245,8 +246,8 @@ def test_ids_past_the_vocabulary(dev):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("order", ["ascending", "descending", "equal", "few values"])
-@pytest.mark.parametrize("V", [900, 20000, 140001])
-def test_top_alternatives_of_ordered_rows(dev, V, order, dtype):
+@pytest.mark.parametrize("V,T", [(900, 2), (20000, 2), (140001, 2), (3000, 600)])
+def test_top_alternatives_of_ordered_rows(dev, V, T, order, dtype):
     v = torch.linspace(-4, 4, V, device=dev).to(dtype)
     if order == "descending":
         v = v.flip(0)
@@ -255,8 +256,8 @@ def test_top_alternatives_of_ordered_rows(dev, V, order, dtype):
         v[7::3] = 0.0
     elif order == "few values":
         v = (torch.randint(0, 4, (V,), device=dev) - 2).to(dtype)
-    logits = torch.stack([v, v.roll(777)])
-    ids = torch.tensor([0, V - 1], device=dev)
+    logits = torch.stack([v.roll(777 * t) for t in range(T)])
+    ids = torch.arange(T, device=dev) * (V - 1) % V
     got = R.token_logprobs(logits, ids, top=32)
     check_forward(logits, ids, 1.0, got, 32)
 
