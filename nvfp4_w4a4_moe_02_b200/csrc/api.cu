@@ -1309,7 +1309,7 @@ nvfp4_status token_logprobs_backward(const void* logits, nvfp4_dtype dtype, int6
     return fail(NVFP4_ERR_INVALID_ARG, "in place needs ldg == ldl");
   LogprobBwdArgs a{logits, T, V, ldl, dtype == NVFP4_OUT_BF16, ids, id_bytes, inv_temperature, stats, grad_logprob,
                    grad_entropy, grad_logits, ldg, dev_status};
-  cudaError_t e = launch_logprobs_backward(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_logprobs_backward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "log probability backward launch");
 }
 

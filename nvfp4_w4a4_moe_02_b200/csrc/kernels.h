@@ -285,7 +285,7 @@ struct LogprobBwdArgs {
   int64_t ldg;
   int32_t* status;
 };
-cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t st);
+cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st);
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, int32_t* status, cudaStream_t st);
 

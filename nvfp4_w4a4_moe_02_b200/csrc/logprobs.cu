@@ -733,8 +733,10 @@ cudaError_t launch_forward(const LogprobArgs& a, int num_sms, cudaStream_t st) {
 }
 
 template <typename L>
-cudaError_t launch_backward(const LogprobBwdArgs& a, cudaStream_t st) {
-  if (a.V <= kWarpRow) {
+cudaError_t launch_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
+  // a warp a row where a block would not fill its stretch and the rows fill the card (us, warp against
+  // block: 4000 x 1500 bf16 5.1, 12.6; 4000 x 8000 21.3, 24.0; 300 x 3000 f32 5.1, 3.2)
+  if (a.V <= kWarpRow || (a.V <= 8 * kWarpRow && a.T >= 8 * (int64_t)num_sms)) {
     logprobs_backward_kernel<L, 1><<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>(a, 1);
     return cudaGetLastError();
   }
@@ -753,8 +755,8 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t st) 
   return a.k_top > 0 ? launch_forward<float, true>(a, num_sms, st) : launch_forward<float, false>(a, num_sms, st);
 }
 
-cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t st) {
-  return a.bf16 ? launch_backward<uint16_t>(a, st) : launch_backward<float>(a, st);
+cudaError_t launch_logprobs_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t st) {
+  return a.bf16 ? launch_backward<uint16_t>(a, num_sms, st) : launch_backward<float>(a, num_sms, st);
 }
 
 }  // namespace nvfp4
