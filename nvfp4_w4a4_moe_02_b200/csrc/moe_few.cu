@@ -63,29 +63,33 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Asynchronous 16-byte copies; weights past L1, activations through it.
+// Asynchronous copies of 16, 8 or 4 bytes to smem + OFF; weights past L1, activations through it.
+template <int OFF>
 __device__ __forceinline__ void copy16_stream(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(smem), "l"(gmem), "n"(OFF) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
+template <int OFF, int BYTES>
+__device__ __forceinline__ void copy_act(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0 + %2], [%1], %3;" ::"r"(smem), "l"(gmem), "n"(OFF), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+template <int OFF>
 __device__ __forceinline__ uint4 lds16(uint32_t smem) {
   uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(smem) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4 + %5];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(smem), "n"(OFF)
+               : "memory");
   return r;
 }
+template <int OFF>
 __device__ __forceinline__ float2 lds8(uint32_t smem) {
   float2 r;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(smem) : "memory");
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2 + %3];" : "=f"(r.x), "=f"(r.y) : "r"(smem), "n"(OFF) : "memory");
   return r;
 }
 
@@ -96,6 +100,17 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void load_b(uint32_t (&b)[16], const uint4& p, const uint4& q, const uint4& r, const uint4& s) {
+  const uint4 v[4] = {p, q, r, s};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    b[4 * i] = v[i].x;
+    b[4 * i + 1] = v[i].y;
+    b[4 * i + 2] = v[i].z;
+    b[4 * i + 3] = v[i].w;
+  }
 }
 
 // The byte `I` of a word of codes -> two halves.  The conversion reads its register's low byte.
@@ -430,10 +445,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
   const int my_chunks = (nch - part + S - 1) / S;  // at least one: S <= nch
 
   // ---- the copying side, kSteps steps ahead
-  int cu = u, cc = 0, cpair = 0;  // unit, chunk (of this warp's), pair
-  uint32_t cstep = 0, cact = 0;   // offsets of the ring's next places
+  const int64_t row32 = 16 * (int64_t)cols;  // bytes of 32 rows
+  const uint32_t sf_to = 2048 + 32 * g + 8 * t - 16 * lane;
+  int cu = u, cc = 0;             // unit, chunk (of this warp's)
+  uint32_t cstep = base + 16 * lane, cact = acts + 16 * lane;  // the lane's places in the ring
   const uint8_t *pc = nullptr, *ps = nullptr;
-  const uint8_t *pa = nullptr, *pas = nullptr;  // the lane's activations of chunk 0, their scales
+  const uint8_t *pa = nullptr, *pas = nullptr;  // the lane's activations of the chunk, their scales
   bool col = false;
   auto enter = [&](int unit) {
     const int slot = unit / groups, grp = unit % groups;
@@ -450,37 +467,31 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
     pas = reinterpret_cast<const uint8_t*>(UP ? a.x_scale + r * (cols / 128) + part
                                               : a.h_scale + r * (cols / 32) + 2 * (t >> 1) + 4 * part);
   };
-  auto copy_step = [&]() {
+  // the first pair of a chunk brings the activations with it
+  auto copy_step = [&](auto second) {
     if (cu < u_end) {
-      const int k0 = 128 * (part + S * cc);
       // past the last 64 columns the lane reads those before them, against activations of zero
-      const bool in = UP || k0 + 32 * t < cols;
+      const bool in = UP || 128 * (part + S * cc) + 32 * t < cols;
       const uint8_t* q = pc + (in ? 0 : -32);
-      const uint32_t dst = base + cstep;
-      const int64_t row8 = 4 * (int64_t)cols;  // bytes of eight rows
-      copy16_stream(dst + 16 * lane, q);
-      copy16_stream(dst + 16 * lane + 512, q + 4 * row8);
-      copy16_stream(dst + 16 * lane + 1024, q + 8 * row8);
-      copy16_stream(dst + 16 * lane + 1536, q + 12 * row8);
-      if ((t & 1) == 0) copy16_stream(dst + 2048 + 32 * g + 8 * t, ps + (in ? 0 : -512));
-      if (cpair == 0) {
+      copy16_stream<0>(cstep, q);
+      copy16_stream<512>(cstep, q += row32);
+      copy16_stream<1024>(cstep, q += row32);
+      copy16_stream<1536>(cstep, q += row32);
+      if ((t & 1) == 0) copy16_stream<0>(cstep + sf_to, ps + (in ? 0 : -512));
+      if constexpr (!second.value) {
         if (col && in) {
-          const uint32_t adst = acts + cact;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) copy16(adst + 512 * i + 16 * lane, pa + 16 * i);
-          if (UP)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(adst + 2048 + 8 * lane), "l"(pas) : "memory");
-          else
-            copy8(adst + 2048 + 8 * lane, pas);
+          copy_act<0, 16>(cact, pa);
+          copy_act<512, 16>(cact, pa + 16);
+          copy_act<1024, 16>(cact, pa + 32);
+          copy_act<1536, 16>(cact, pa + 48);
+          copy_act<2048, UP ? 4 : 8>(cact - 8 * lane, pas);
         }
-        cact ^= kActBytes;
-        cpair = 1;
-        pc += row8;
+        cact = cact >= acts + kActBytes ? cact - kActBytes : cact + kActBytes;
+        pc += row32 / 4;
         ps += 128;
       } else {
-        cpair = 0;
         ++cc;
-        pc += 64 * S - row8;
+        pc += 64 * S - row32 / 4;
         ps += 1024 * S - 128;
         pa += 256 * S;
         pas += (UP ? 4 : 16) * S;
@@ -489,15 +500,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
           if (++cu < u_end) enter(cu);
         }
       }
-      cstep = cstep == (kSteps - 1) * kStepBytes ? 0 : cstep + kStepBytes;
+      cstep = cstep >= base + (kSteps - 1) * kStepBytes ? cstep - (kSteps - 1) * kStepBytes : cstep + kStepBytes;
     }
     copies_commit();
   };
+  static_assert(kSteps == 3, "a chunk's first step is read as a second one is copied");
   enter(u);
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) copy_step();
+  copy_step(std::false_type{});
+  copy_step(std::true_type{});
+  copy_step(std::false_type{});
 
-  uint32_t step = 0, act = 0;
+  uint32_t step = base + 16 * lane, act = acts;
+  const uint32_t sf_from = 2048 + 32 * g + 16 * (t >> 1) - 16 * lane;
   float* red = reinterpret_cast<float*>(smem + kWarps * kWarpBytes);
   for (; u < u_end; ++u) {
     const int slot = u / groups, grp = u % groups;
@@ -509,27 +523,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
       for (int i = 0; i < my_chunks; ++i) {
         uint32_t b[16] = {};
         float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
+        auto pair = [&](auto which) {
+          constexpr int pr = which.value;
           copies_wait<kSteps - 1>();
           __syncwarp();  // the scales of a row are copied by one lane and read by two
-          const uint32_t src = base + step;
-          const uint4 lo0 = lds16(src + 16 * lane), lo1 = lds16(src + 16 * lane + 512);
-          const uint4 hi0 = lds16(src + 16 * lane + 1024), hi1 = lds16(src + 16 * lane + 1536);
-          const uint4 sf = lds16(src + 2048 + 32 * g + 16 * (t >> 1));
+          const uint4 lo0 = lds16<0>(step), lo1 = lds16<512>(step);
+          const uint4 hi0 = lds16<1024>(step), hi1 = lds16<1536>(step);
+          const uint4 sf = lds16<0>(step + sf_from);
           if (pr == 0) {
             const bool in = UP || 128 * (part + S * i) + 32 * t < cols;
-            const uint32_t from = acts + act;
             if constexpr (few.value) {
               if (in) {
                 const int tok = g & 1;
                 if (t == g >> 1 && tok < cnt) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(from + 512 * q + 16 * (4 * tok + t));
+                  const uint32_t from = act + 64 * tok + 16 * t;
+                  load_b(b, lds16<0>(from), lds16<512>(from), lds16<1024>(from), lds16<1536>(from));
                 }
-                d0 = lds8(from + 2048 + 8 * t);
-                if (cnt > 1) d1 = lds8(from + 2048 + 32 + 8 * t);
+                d0 = lds8<2048>(act + 8 * t);
+                if (cnt > 1) d1 = lds8<2048 + 32>(act + 8 * t);
                 if (UP) {  // one scale per chunk
                   d0.y = d0.x;
                   d1.y = d1.x;
@@ -538,9 +549,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
             } else {
               float2 f = make_float2(0.0f, 0.0f);
               if (g < cnt && in) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(&b[4 * q]) = lds16(from + 512 * q + 16 * lane);
-                f = lds8(from + 2048 + 8 * lane);
+                const uint32_t from = act + 16 * lane;
+                load_b(b, lds16<0>(from), lds16<512>(from), lds16<1024>(from), lds16<1536>(from));
+                f = lds8<2048>(act + 8 * lane);
               }
               float d = f.x;
               if (!UP) {
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
               d0.x = __shfl_sync(0xffffffffu, d, 8 * t);
               d1.x = __shfl_sync(0xffffffffu, d, 8 * t + 4);
             }
-            act ^= kActBytes;
+            act = act == acts ? acts + kActBytes : acts;
           }
           if constexpr (few.value) {
             mma_tile_blocks(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0, d1);
@@ -566,10 +577,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
             mma_tile(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0.x, d1.x);
             mma_tile(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0.x, d1.x);
           }
-          step = step == (kSteps - 1) * kStepBytes ? 0 : step + kStepBytes;
+          step = step >= base + (kSteps - 1) * kStepBytes ? step - (kSteps - 1) * kStepBytes : step + kStepBytes;
           __syncwarp();  // every lane has read the place that is filled next
-          copy_step();
-        }
+          copy_step(std::bool_constant<pr == 0>{});
+        };
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
       }
     };
     if (cnt <= 2) {
