@@ -1173,7 +1173,7 @@ namespace {
 enum { kFewXh, kFewXScale, kFewH, kFewHScale, kFewY, kFewLists, kFewParts };
 size_t few_workspace(int64_t T, int32_t k, int64_t H, int64_t I, size_t (&at)[kFewParts]) {
   const size_t P = (size_t)(T * k);
-  const size_t bytes[kFewParts] = {(size_t)(T * H) * 2, (size_t)(T * (H / 128)) * 4, P * (size_t)I * 2,
+  const size_t bytes[kFewParts] = {(size_t)(T * H) * 2, (size_t)(T * (H / 128)) * 4, P * round_up((size_t)I, 128) * 2,
                                    P * (size_t)(I / 32) * 4, P * (size_t)H * 4,
                                    moe_few_list_words(T, k) * sizeof(int32_t)};
   size_t total = 0;

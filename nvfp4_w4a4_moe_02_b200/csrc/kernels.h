@@ -244,9 +244,9 @@ struct MoeFewArgs {
   uint16_t* out;               // bf16 [T x H], pitch ldo
   int64_t ldo;
   // workspaces
-  uint16_t* xh;                // f16 [T x H]: scaled x
+  uint16_t* xh;                // f16 [T x H]: scaled x, each 128 in the order of the matrix instructions, as h
   float* x_scale;              // [T x H / 128]: the powers of two taken out of x
-  uint16_t* h;                 // f16 [T k x I]: scaled SwiGLU outputs, rows in slot order
+  uint16_t* h;                 // f16 [T k x I rounded up to 128]: scaled SwiGLU outputs, rows in slot order
   float* h_scale;              // [T k x I / 32]
   float* y;                    // [T k x H]: outputs of the pairs, rows in slot order
   int32_t* lists;              // moe_few_list_words(T, k) words
