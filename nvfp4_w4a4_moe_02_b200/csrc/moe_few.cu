@@ -405,10 +405,12 @@ __global__ void __launch_bounds__(1024) moe_few_prepare_kernel(MoeFewArgs a) {
 
 // UP: gate_up + SwiGLU -> h.  Otherwise down: the products of each slot, in binary32, -> y.
 //
-// Units are split evenly over the teams of S warps, in one contiguous run each, slots outermost.  S is the
-// least power of two that gives three quarters of the card's warps a unit, while a warp keeps two chunks; a
-// team's warps take every S-th chunk and join in shared memory (1 token, hidden 7168, us of a call at S = 1,
-// 2, 4, 8, 16: 98.7, 86.0, 64.3, 68.9, 80.0; 64 tokens: 1184, 1222, 1274, 1384, 1685).
+// Units are split evenly over the teams of S warps, in one contiguous run each, slots outermost; a team's
+// warps take every S-th chunk and join in shared memory.  S is the power of two that leaves the busiest warp
+// the fewest chunks, a join counted as one; the least of equals.  (Against the least S that gives three quarters
+// of the warps a unit, us of a call: 32 tokens, hidden 2048, 2 of 16 experts 32.0 -> 27.2; 64 tokens, 8 of 128
+// 117.5 -> 109.1; one token, 8 of 128 21.5 -> 20.5; 64 tokens, hidden 7168, 8 of 256 1100 -> 1086; the smallest
+// calls 13.9 -> 14.0.)
 template <bool UP>
 __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -435,8 +437,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
 
   const int units = n * groups;
   const int warps = gridDim.x * kWarps;
-  int S = 1;
-  while (S < kWarps && 4 * S <= nch && 4 * units * S < 3 * warps) S *= 2;
+  uint32_t rank = 0xFFFFFFFFu;  // lane i weighs S = 2^i
+  if (1 << lane <= min(kWarps, nch)) {
+    const uint32_t teams = (uint32_t)warps >> lane;
+    rank = (((uint32_t)units + teams - 1) / teams * (uint32_t)((nch - 1 >> lane) + 1 + (lane > 0))) << 3 | lane;
+  }
+  const int S = 1 << (__reduce_min_sync(0xffffffffu, rank) & 7u);
   const int team = (blockIdx.x * kWarps + warp) / S, teams = warps / S, part = warp & (S - 1);
   int u = (int)((int64_t)units * team / teams);
   const int u_end = (int)((int64_t)units * (team + 1) / teams);
