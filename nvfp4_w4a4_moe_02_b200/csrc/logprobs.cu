@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
 // takes a stretch of a row, W = 1: a warp takes a row.  16-byte accesses where the row of the logits and
 // of the gradient have the same phase.
 // Eight blocks a SM keep enough bytes on the way for reads and writes together (4096 x 131072 bf16: 397 us
-// at four, 347 us at six, 334 us at eight, 6.4 TB/s).
+// at four, 347 us at six, 334 us at eight; with 32-bit indices in a row 327 us, 6.56 TB/s).
 template <typename L, int W>
 __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(LogprobBwdArgs a, int64_t stretches) {
   constexpr int N = Vec<L>::N;

@@ -856,7 +856,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float =
     logits: float32 or bf16 [T, V], any row pitch; -inf is a masked token.  ids: int32 or int64;
     a negative id marks a padding row (zeros, top_ids -1, no gradient).  logprob and entropy carry
     gradients to the logits; with them, another stream is chosen by making it current, so that the
-    backward pass follows."""
+    backward pass follows.  A captured backward pass needs a leaf that no living eager graph holds:
+    torch adds up a leaf's gradients on the stream of its first graph, which a capture cannot use."""
     if logits.requires_grad and torch.is_grad_enabled():
         if stream is not None:
             _refuse("with gradients, make the stream current instead of passing it")
