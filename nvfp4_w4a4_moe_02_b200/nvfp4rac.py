@@ -685,6 +685,8 @@ class _On:
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device_index != self.index:
+                _refuse(f"the stream is on device {stream.device_index}, the tensors on {self.index}")
             self.ctx = torch.cuda.stream(stream)
         elif self.index != torch.cuda.current_device():
             self.ctx = torch.cuda.device(device)

@@ -107,3 +107,14 @@ def test_binding_refuses_host_tensors(lib):
     p = R.Packed(torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8), torch.zeros(4), 4, 256, 256, 256)
     with pytest.raises(R.NVFP4Error):
         R.moe_w4a16_layer(torch.zeros(1, 256, dtype=torch.bfloat16), torch.zeros(1, 4), 2, p, p)
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+
+    import torch
+    from nvfp4_w4a4_moe_02_b200 import nvfp4rac as R
+
+    stream = types.SimpleNamespace(cuda_stream=16, device_index=1)
+    with pytest.raises(R.NVFP4Error, match="device 1"):
+        R._On(torch.device("cuda", 0), stream)
