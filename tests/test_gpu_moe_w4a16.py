@@ -102,6 +102,20 @@ def test_layer_matches_64_bits(dev, T, H, I, E, k):
     check(x, logits, k, pgu, pdn, out, ids, w, st)
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [
+    (1, 2048, 64, 4, 2),       # a block's sixteen warps on one unit; the down projection half a chunk
+    (1, 1152, 1152, 4, 2),     # eight warps on nine chunks
+    (3, 1280, 1344, 4, 2),     # eight on ten, and on eleven of which the last is a half
+    (64, 512, 1600, 2, 2),     # two on four in gate_up, eight on thirteen with a half
+    (64, 128, 32768, 2, 2),    # one chunk against the longest down projection
+])
+def test_k_split_over_warps(dev, T, H, I, E, k):
+    x, logits, pgu, pdn = make_layer(dev, T, H, I, E, k, seed=I)
+    st = R.new_status(dev)
+    out, ids, w = R.moe_w4a16_layer(x, logits, k, pgu, pdn, status=st)
+    check(x, logits, k, pgu, pdn, out, ids, w, st)
+
+
 @pytest.mark.parametrize("T", range(2, 24, 3))
 def test_token_counts(dev, T):
     x, logits, pgu, pdn = make_layer(dev, T, 256, 192, 5, 2, seed=T)
