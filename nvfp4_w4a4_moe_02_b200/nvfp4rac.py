@@ -674,34 +674,26 @@ def grouped_w4a4_rac_moe_combine(a: Packed, a_res: Packed | None, expert_offsets
     return out
 
 
-class _On:
-    """Makes the tensors' device current and `stream` (None: that device's current stream) the one
-    that buffers are allocated on and kernels are launched on."""
+def _on(device: torch.device, stream=None):
+    """A context with the tensors' device current and `stream` (None: that device's current stream) the
+    one that buffers are allocated on and kernels are launched on."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device_index != device.index:
+        _refuse(f"the stream is on device {stream.device_index}, the tensors on {device.index}")
+    return torch.cuda.stream(stream)
 
-    __slots__ = ("ctx", "index")
 
-    def __init__(self, device: torch.device, stream=None):
-        self.index = device.index
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device_index != self.index:
-                _refuse(f"the stream is on device {stream.device_index}, the tensors on {self.index}")
-            self.ctx = torch.cuda.stream(stream)
-        elif self.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-        else:
-            self.ctx = None
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Whether a call needs _on: the ordinary one takes what is current (a context costs 0.5 us)."""
+    return stream is not None or device.index != torch._C._cuda_getDevice()
 
-    def __enter__(self) -> int:
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        # the handle alone: a Stream object costs as much as a launch
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _raw_stream(device: torch.device) -> int:
+    """The handle alone: a Stream object costs as much as a launch."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _refuse(text: str):
@@ -744,17 +736,19 @@ def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Pa
         _refuse("out must be bf16 [T, H] with unit column stride on x's device")
     if workspace is not None and not (workspace.is_contiguous() and workspace.device == dev):
         _refuse("workspace must be contiguous on x's device")
-    with _On(dev, stream) as s:
-        ids = torch.empty(T, k, dtype=torch.int32, device=dev) if ids is None else ids
-        w = torch.empty(T, k, dtype=torch.float32, device=dev) if w is None else w
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
-        if workspace is None:
-            workspace = torch.empty(lib.moe_w4a16_workspace_size(T, k, H, I), dtype=torch.uint8, device=dev)
-        gu, dn = w_gate_up.c(), w_down.c()
-        _check(lib.moe_w4a16_layer(x.data_ptr(), T, x.stride(0) if T > 1 else H, logits.data_ptr(), k,
-                                   ctypes.byref(gu), ctypes.byref(dn), ids.data_ptr(), w.data_ptr(), out.data_ptr(),
-                                   out.stride(0) if T > 1 else H, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _ptr(status), s))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_w4a16_layer(x, logits, k, w_gate_up, w_down, ids, w, out, workspace, status)
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev) if ids is None else ids
+    w = torch.empty(T, k, dtype=torch.float32, device=dev) if w is None else w
+    out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+    if workspace is None:
+        workspace = torch.empty(lib.moe_w4a16_workspace_size(T, k, H, I), dtype=torch.uint8, device=dev)
+    gu, dn = w_gate_up.c(), w_down.c()
+    _check(lib.moe_w4a16_layer(x.data_ptr(), T, x.stride(0) if T > 1 else H, logits.data_ptr(), k,
+                               ctypes.byref(gu), ctypes.byref(dn), ids.data_ptr(), w.data_ptr(), out.data_ptr(),
+                               out.stride(0) if T > 1 else H, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _ptr(status), _raw_stream(dev)))
     return out, ids, w
 
 
@@ -789,16 +783,18 @@ def _logprobs_forward(logits, ids, temperature, top, status, stream, want_stats)
     if not (isinstance(top, int) and 0 <= top <= min(32, V)):
         _refuse("top must be in [0, min(32, V)]")
     dev = logits.device
-    with _On(dev, stream) as s:
-        logprob = torch.empty(T, dtype=torch.float32, device=dev)
-        entropy = torch.empty(T, dtype=torch.float32, device=dev)
-        stats = torch.empty(T, 4, dtype=torch.float32, device=dev) if want_stats else None
-        top_ids = top_lp = None
-        if top:
-            top_ids = torch.empty(T, top, dtype=torch.int32, device=dev)
-            top_lp = torch.empty(T, top, dtype=torch.float32, device=dev)
-        _check(load().token_logprobs(*args, top, logprob.data_ptr(), entropy.data_ptr(), _ptr(stats), _ptr(top_ids),
-                                     _ptr(top_lp), _ptr(status), s))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _logprobs_forward(logits, ids, temperature, top, status, None, want_stats)
+    logprob = torch.empty(T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    stats = torch.empty(T, 4, dtype=torch.float32, device=dev) if want_stats else None
+    top_ids = top_lp = None
+    if top:
+        top_ids = torch.empty(T, top, dtype=torch.int32, device=dev)
+        top_lp = torch.empty(T, top, dtype=torch.float32, device=dev)
+    _check(load().token_logprobs(*args, top, logprob.data_ptr(), entropy.data_ptr(), _ptr(stats), _ptr(top_ids),
+                                 _ptr(top_lp), _ptr(status), _raw_stream(dev)))
     return logprob, entropy, stats, top_ids, top_lp
 
 
@@ -817,10 +813,13 @@ def token_logprobs_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torc
     if out is not None and not (out.shape == (T, V) and out.dtype == logits.dtype and (V == 1 or out.stride(1) == 1)
                                 and (T <= 1 or out.stride(0) >= V) and out.device == dev):
         _refuse("out must be a matrix like the logits")
-    with _On(dev, stream) as s:
-        out = torch.empty(T, V, dtype=logits.dtype, device=dev) if out is None else out
-        _check(load().token_logprobs_backward(*args, stats.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
-                                              out.data_ptr(), out.stride(0) if T > 1 else V, _ptr(status), s))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return token_logprobs_backward(logits, ids, stats, temperature, grad_logprob, grad_entropy, out, status)
+    out = torch.empty(T, V, dtype=logits.dtype, device=dev) if out is None else out
+    _check(load().token_logprobs_backward(*args, stats.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
+                                          out.data_ptr(), out.stride(0) if T > 1 else V, _ptr(status),
+                                          _raw_stream(dev)))
     return out
 
 

@@ -117,4 +117,4 @@ def test_a_stream_of_another_device_is_refused():
 
     stream = types.SimpleNamespace(cuda_stream=16, device_index=1)
     with pytest.raises(R.NVFP4Error, match="device 1"):
-        R._On(torch.device("cuda", 0), stream)
+        R._on(torch.device("cuda", 0), stream)
