@@ -29,13 +29,14 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "moe_few_split.h"
 
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kSlot = 8;                        // tokens of a slot
-constexpr int kWarps = 16;                      // warps of a block, one block a SM
+constexpr int kWarps = kFewWarps;               // warps of a block, one block a SM
 constexpr int kTiles = 4;                       // 16-row tiles of a unit: two pairs
 constexpr int kSteps = 3;                       // depth of the ring; a step is a pair's 128 columns
 constexpr int kStepBytes = 4 * 512 + 256;       // codes: [4][32 lanes] x 16 bytes, scales: [16] x 16 bytes
@@ -441,11 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
 
   const int units = n * groups;
   const int warps = gridDim.x * kWarps;
-  uint32_t rank = 0xFFFFFFFFu;  // lane i weighs S = 2^i
-  if (1 << lane <= min(kWarps, nch)) {
-    const uint32_t teams = (uint32_t)warps >> lane;
-    rank = (((uint32_t)units + teams - 1) / teams * (uint32_t)((nch - 1 >> lane) + 1 + (lane > 0))) << 3 | lane;
-  }
+  const uint32_t rank = few_split_cost(lane, units, warps, nch);  // lane i weighs S = 2^i
   const int S = 1 << (__reduce_min_sync(0xffffffffu, rank) & 7u);
   const int team = (blockIdx.x * kWarps + warp) / S, teams = warps / S, part = warp & (S - 1);
   int u = (int)((int64_t)units * team / teams);
