@@ -15,6 +15,7 @@
 // logit is not above kLow (masked by the type's lowest value, or all -inf) is done again exactly.
 #include "common.cuh"
 #include "kernels.h"
+#include "logprobs_index.h"
 
 namespace nvfp4 {
 
@@ -645,8 +646,8 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   };
   const Span<L> sp(row, (int)a.V, 0, 1);
   if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grow)) & 15) != 0) {
-    const int end = (int)(a.V * (at + 1) / stretches);
-    for (int v = (int)(a.V * at / stretches) + tid; v < end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
+    const ElementRange r = stretch_elements(a.V, at, stretches);
+    for (auto v = r.first + tid; v < r.end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), (int)v));
     return;
   }
   uint4* gvec = reinterpret_cast<uint4*>(grow + sp.head);
@@ -740,9 +741,7 @@ cudaError_t launch_backward(const LogprobBwdArgs& a, int num_sms, cudaStream_t s
     logprobs_backward_kernel<L, 1><<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>(a, 1);
     return cudaGetLastError();
   }
-  // four vectors a thread, more where the grid would pass its limit
-  int64_t stretches = (a.V + 1024 * Vec<L>::N - 1) / (1024 * Vec<L>::N);
-  if (stretches > INT32_MAX / a.T) stretches = INT32_MAX / a.T;
+  const int64_t stretches = logprob_stretches(a.T, a.V, Vec<L>::N);
   logprobs_backward_kernel<L, 8><<<(unsigned)(a.T * stretches), 256, 0, st>>>(a, stretches);
   return cudaGetLastError();
 }

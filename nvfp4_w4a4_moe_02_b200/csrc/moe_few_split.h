@@ -1,12 +1,6 @@
 // How the few-token layer's streaming kernels split K: plain arithmetic, the same on the host.
 #pragma once
-#include <stdint.h>
-
-#ifdef __CUDACC__
-#define NVFP4_HOST_DEVICE __host__ __device__ __forceinline__
-#else
-#define NVFP4_HOST_DEVICE inline
-#endif
+#include "host_device.h"
 
 namespace nvfp4 {
 
