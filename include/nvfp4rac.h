@@ -472,8 +472,12 @@ nvfp4_status grouped_w4a4_rac_moe_combine(const nvfp4_tensor* a, const nvfp4_ten
 /* by quantising them, no residual is needed (W_sel is not read), and the function is the      */
 /* trainer's own ("Two fixes": Asymmetric QAT quantises the weights only).                     */
 /*   (ids, w)_t as moe_route_topk;  h = silu(G x) * (U x);  out_t = bf16(sum_j w_tj D h_tj)     */
-/*   with the packed weights' values e * S * s_g; binary32 sums, one rounding at the end, h held */
-/*   with 11 significant bits or more.  The result does not depend on timing.                   */
+/*   with the packed weights' values e * S * s_g; binary32 sums, one rounding at the end.       */
+/*   x is exact down to 2^-31 of the largest magnitude of its aligned 128 columns, and smaller  */
+/*   elements to 2^-39 of that.  h has 11 significant bits down to 2^-15 of the largest of its   */
+/*   32 (in each aligned 64 of a row 0-15 with 32-47, 16-31 with 48-63), whatever the others of  */
+/*   its row, and smaller elements to 2^-26 of that; below 2^-100 the 32's largest counts as     */
+/*   2^-100.  The result does not depend on timing.                                              */
 /*   x           bf16 [T x H], pitch ldx (>= H, a multiple of 8), 16-byte aligned.              */
 /*   logits      float32 [T x E], contiguous.  A token with an infinity or NaN among them gets   */
 /*               ids -1, weights 0 and a zero row, and NVFP4_ERR_RANGE goes to *dev_status.      */

@@ -16,7 +16,9 @@
 //     by a quad takes 64 bytes together (64 tokens in each of 4 experts: 73.1 -> 70.7 us).
 //   - Activations are f16 with a power of two per token and stretch that brings the stretch's largest
 //     to [2^14, 2^15): x per 128 elements, which keeps every bf16 down to 2^-31 of the largest exact;
-//     h, kept with 11 bits, per 32.  The powers are taken out of a chunk's sum.
+//     h, kept with 11 bits (an eighth of the output's own rounding; binary32 would be three f16 products
+//     in the place of one), per 32.  The powers are taken out of a chunk's sum; where those of h lie far
+//     apart, the chunk takes a product for each magnitude.
 //   - A scale atom's 16 bytes j hold the scales of rows j, 32 + j, 64 + j, 96 + j of its 128.  Tiles go in
 //     pairs over eight j: the first takes rows j and 64 + j, the second rows 32 + j and 96 + j, so that one
 //     16-byte load brings a lane the scales of both tiles.  In the gate/up interleaved pack rows 0 .. 63
@@ -209,6 +211,17 @@ __device__ __forceinline__ void stretch_scale(int e, float* up, float* down) {
   e = min(max(e, 27), 254);
   *up = __uint_as_float((uint32_t)(268 - e) << 23);
   *down = __uint_as_float((uint32_t)(e - 26) << 23);
+}
+
+// Stretches of a chunk whose scale is not below kNear of the largest are brought to it by an f16 quotient; the
+// others go in further products of their own, so that an element keeps its 11 bits down to 2^-15 of the largest
+// of its 32.
+constexpr float kNear = 1.220703125e-4f;  // 2^-13
+// The largest scale of a column's chunk, from the two of each lane of the quad.
+__device__ __forceinline__ float quad_max(float2 f) {
+  float d = fmaxf(f.x, f.y);
+  d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
+  return fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2));
 }
 
 // The kernels of a call overlap their launches: a kernel lets the next one start early, and that
@@ -551,6 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
       for (int i = 0; i < my_chunks; ++i) {
         uint32_t b[16] = {};
         float2 d0 = make_float2(0.0f, 0.0f), d1 = d0;
+        bool rest = false;  // stretches far below their chunk's largest are left
         auto pair = [&](auto which) {
           constexpr int pr = which.value;
           copies_wait<kSteps - 1>();
@@ -585,11 +599,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
               if (!UP) {
                 // one scale per column and chunk: the largest; the others' elements take the quotient (a
                 // power of two).  Of the lane's 32 elements the first and the second 16 have a scale each.
-                d = fmaxf(fmaxf(f.x, f.y), 1.17549435e-38f);
-                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
-                d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2));
-                const float inv = __uint_as_float(0x7F000000u - __float_as_uint(d));
-                const uint32_t q0 = pack_f16(f.x * inv, f.x * inv), q1 = pack_f16(f.y * inv, f.y * inv);
+                d = quad_max(f);
+                const float inv = __uint_as_float(0x7F000000u - __float_as_uint(fmaxf(d, 1.17549435e-38f)));
+                const bool late0 = f.x < d * kNear, late1 = f.y < d * kNear;
+                const uint32_t q0 = late0 ? 0u : pack_f16(f.x * inv, f.x * inv);
+                const uint32_t q1 = late1 ? 0u : pack_f16(f.y * inv, f.y * inv);
+                rest = __any_sync(0xffffffffu, (late0 && f.x > 0.0f) || (late1 && f.y > 0.0f));
 #pragma unroll
                 for (int q = 0; q < 16; ++q) b[q] = hmul2(b[q], q < 8 ? q0 : q1);
               }
@@ -604,6 +619,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
           } else {
             mma_tile(acc[2 * pr], lo0, hi0, sf.x, sf.z, b, d0.x, d1.x);
             mma_tile(acc[2 * pr + 1], lo1, hi1, sf.y, sf.w, b, d0.x, d1.x);
+            if constexpr (!UP) {
+              if (rest) {
+                // the chunk's activations are still where they were; act has gone on to the next
+                const uint32_t from = (act == acts ? acts + kActBytes : acts) + 16 * lane;
+                float2 f = make_float2(0.0f, 0.0f);
+                if (g < cnt && 128 * (part + S * i) + 32 * t < cols) f = lds8<2048>(from - 8 * lane);
+                float d = quad_max(f);
+#pragma unroll 1
+                while (true) {
+                  // those taken so far are out; the next ones are those near the largest that is left
+                  if (f.x >= d * kNear) f.x = 0.0f;
+                  if (f.y >= d * kNear) f.y = 0.0f;
+                  if (!__any_sync(0xffffffffu, f.x + f.y > 0.0f)) break;
+                  d = quad_max(f);
+                  const float inv = __uint_as_float(0x7F000000u - __float_as_uint(fmaxf(d, 1.17549435e-38f)));
+                  const float qx = f.x < d * kNear ? 0.0f : f.x * inv, qy = f.y < d * kNear ? 0.0f : f.y * inv;
+                  const uint32_t q0 = pack_f16(qx, qx), q1 = pack_f16(qy, qy);
+                  uint32_t c[16] = {};
+                  if (f.x + f.y > 0.0f) {
+                    load_b(c, lds16<0>(from), lds16<512>(from), lds16<1024>(from), lds16<1536>(from));
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) c[q] = hmul2(c[q], q < 8 ? q0 : q1);
+                  }
+                  const float e0 = __shfl_sync(0xffffffffu, d, 8 * t), e1 = __shfl_sync(0xffffffffu, d, 8 * t + 4);
+                  // the codes are read again, so that nothing is kept in registers for this
+                  const uint4 s4 = lds16<0>(step + sf_from);
+                  mma_tile(acc[2 * pr], lds16<0>(step), lds16<1024>(step), s4.x, s4.z, c, e0, e1);
+                  mma_tile(acc[2 * pr + 1], lds16<512>(step), lds16<1536>(step), s4.y, s4.w, c, e0, e1);
+                }
+              }
+            }
           }
           step = step >= base + (kSteps - 1) * kStepBytes ? step - (kSteps - 1) * kStepBytes : step + kStepBytes;
           __syncwarp();  // every lane has read the place that is filled next
@@ -677,7 +723,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
 #pragma unroll
           for (int r = 0; r < kTiles; ++r)
             o[8 * (r & 1) + 32 * (r >> 1)] = __half_as_ushort(__float2half_rn(h[r][j] * up));
-          if (g == 0) a.h_scale[p * (a.I / 32) + grp] = down;
+          if (g == 0) a.h_scale[p * (a.I / 32) + grp] = top == 0 ? 0.0f : down;
         }
       }
     } else {
