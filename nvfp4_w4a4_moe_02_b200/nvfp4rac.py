@@ -17,6 +17,7 @@ from dataclasses import dataclass
 from typing import NamedTuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libnvfp4rac.so")
@@ -700,6 +701,11 @@ def _refuse(text: str):
     raise NVFP4Error(1, text)
 
 
+def _no_tangent(t: torch.Tensor, name: str):
+    if unpack_dual(t).tangent is not None:
+        _refuse(f"{name} carries a forward-mode tangent, which has no formula here")
+
+
 def _check_like(t, shape, dtype, device, name: str):
     if t is not None and not (t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == device):
         _refuse(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
@@ -714,8 +720,13 @@ def moe_w4a16_layer(x: torch.Tensor, logits: torch.Tensor, k: int, w_gate_up: Pa
     Weights as the other paths use them: w_gate_up from pack_weights(gate_up_interleave=True)
     [E, 2I, H], w_down from pack_weights [E, H, I].  Activations are not quantised: the layer is the
     trainer's function of fake-quantised weights.  `workspace` (uint8, moe_w4a16_workspace_size
-    bytes) is allocated per call unless given; calls that may overlap need their own."""
+    bytes) is allocated per call unless given; calls that may overlap need their own.  There is no
+    gradient: x or logits that ask for one are refused (call it under torch.no_grad() or detach them)."""
     lib = load()
+    if (x.requires_grad or logits.requires_grad) and torch.is_grad_enabled():
+        _refuse("the layer has no gradient: detach x and logits, or call it under torch.no_grad()")
+    _no_tangent(x, "x")
+    _no_tangent(logits, "logits")
     if not (x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.stride(1) == 1):
         _refuse("x must be a bf16 CUDA matrix with unit column stride")
     T, H = x.shape
@@ -858,11 +869,13 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, temperature: float =
     a negative id marks a padding row (zeros, top_ids -1, no gradient).  logprob and entropy carry
     gradients to the logits; with them, another stream is chosen by making it current, so that the
     backward pass follows.  A captured backward pass needs a leaf that no living eager graph holds:
-    torch adds up a leaf's gradients on the stream of its first graph, which a capture cannot use."""
+    torch adds up a leaf's gradients on the stream of its first graph, which a capture cannot use.
+    Forward-mode tangents are refused."""
     if logits.requires_grad and torch.is_grad_enabled():
         if stream is not None:
             _refuse("with gradients, make the stream current instead of passing it")
         return TokenLogprobs(*_TokenLogprobsFn.apply(logits, ids, temperature, top, status))
+    _no_tangent(logits, "logits")
     lp, ent, _, ti, tl = _logprobs_forward(logits, ids, temperature, top, status, stream, False)
     return TokenLogprobs(lp, ent, ti, tl)
 
