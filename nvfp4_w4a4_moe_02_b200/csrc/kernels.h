@@ -266,7 +266,7 @@ struct LogprobArgs {
   int32_t k_top;
   float* logprob;              // [T]
   float* entropy;              // optional [T]
-  float* stats;                // optional [T x 4]: max logit, its reference M, log2 of the sum, entropy
+  float* stats;                // optional [T x 4]: max logit, 1 / s and log2 s of the sum s, entropy
   int32_t* top_ids;            // [T x k_top]
   float* top_lp;               // [T x k_top]
   int32_t* status;

@@ -162,7 +162,7 @@ __device__ __forceinline__ void add_vectors(Stat& a, uint4 (&r)[U], float c) {
   for (int i = 1; i < U; ++i) bm = fmaxf(bm, Vec<L>::clamp(r[i], low));
   if (!(bm <= a.m)) {
     a.m = fmaxf(a.m, bm);
-    if (a.m > kLow) rebase(a, a.m * c);
+    if (a.m > kLow) rebase(a, __fmul_rn(a.m, c));
   }
   // while nothing is above kLow the elements are skipped: they add nothing to a row that has more, and
   // the others are done again; a NaN must not be lost
@@ -190,7 +190,7 @@ __device__ __forceinline__ void add_element(Stat& a, float x, float c) {
   if (x != x) a.s = x;
   if (x > a.m) {
     a.m = x;
-    if (x > kLow) rebase(a, x * c);
+    if (x > kLow) rebase(a, __fmul_rn(x, c));
   }
   if (a.M > -INFINITY) {
     const float y = fmaf(fmaxf(x, kLow), c, -a.M);
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(W > 1 ? W * 32 : 256) logprobs_kernel(LogprobA
     const float h = empty ? 0.0f : bad ? NAN : fmaxf((ls - st.u / st.s) * kLn2, 0.0f);
     a.logprob[t] = bad ? NAN : log_prob(l_id);
     if (a.entropy) a.entropy[t] = h;
-    if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(bad ? NAN : st.m, st.M, ls, h);
+    if (a.stats) reinterpret_cast<float4*>(a.stats)[t] = make_float4(bad ? NAN : st.m, empty ? 0.0f : 1.0f / st.s, ls, h);
   }
   if (TOP && place < k && key != 0) {
     a.top_ids[t * k + place] = key_index(key);
@@ -613,33 +613,34 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   const L* row = reinterpret_cast<const L*>(a.logits) + t * a.ld;
   L* grow = reinterpret_cast<L*>(a.grad) + t * a.ldg;
   int64_t id = read_id(a.ids, a.id_bytes, t);
-  const float4 st = __ldg(reinterpret_cast<const float4*>(a.stats) + t);  // m, M, log2 s, entropy
+  const float4 st = __ldg(reinterpret_cast<const float4*>(a.stats) + t);  // m, 1 / s, log2 s, entropy
   if (id >= a.V) {
     if (tid == 0 && at == 0) report_status(a.status, kErrInvalid);
     id = -1;
   }
   const float c = a.inv_temp * kLog2e;
   const bool zero = id < 0 || st.x == -INFINITY;
-  const bool exact = needs_exact(st.x, st.y);
+  const float M = __fmul_rn(st.x, c);  // as the forward pass took it
+  const bool exact = needs_exact(st.x, M);
   float ga = 0.0f, gb = 0.0f;
   if (!zero) {
     if (a.g_lp) ga = __ldg(a.g_lp + t) * a.inv_temp;
     if (a.g_ent) gb = __ldg(a.g_ent + t) * a.inv_temp;
   }
-  const float rs = ex2(-st.z);
+  const float rs = st.y;  // 2^-log2(s) would carry log2's rounding, 7e-7 of p at 100000 logits
   const float A = -rs * fmaf(gb, fmaf(st.z, -kLn2, st.w), ga), B = -rs * gb * kLn2;
   // logits whose 2^y is 0 many times over count as this: A + B y stays finite
-  const float floor_l = (st.y - 16384.0f) / c;
+  const float floor_l = (M - 16384.0f) / c;
   const uint32_t low = Vec<L>::bound(floor_l);
   const int at_id = (int)id;
   auto element = [&](float l, int v) {
     if (zero) return 0.0f;
     float g;
     if (exact) {
-      const float q = fmaxf((l - st.x) * c - st.z, -1000.0f);  // log2 p
-      g = -ex2(q) * fmaf(gb, fmaf(q, kLn2, st.w), ga) + (st.x - st.x);
+      const float y = fmaxf((l - st.x) * c, -1000.0f);
+      g = -rs * ex2(y) * fmaf(gb, fmaf(y - st.z, kLn2, st.w), ga) + (st.x - st.x);
     } else {
-      const float y = fmaf(l < floor_l ? floor_l : l, c, -st.y);
+      const float y = fmaf(l < floor_l ? floor_l : l, c, -M);
       g = ex2(y) * fmaf(B, y, A);
     }
     return v == at_id ? g + ga : g;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   }
   uint4* gvec = reinterpret_cast<uint4*>(grow + sp.head);
   const int lo = (int)(sp.hi * at / stretches), hi = (int)(sp.hi * (at + 1) / stretches);
-  const float2 c2 = make_float2(c, c), M2 = make_float2(-st.y, -st.y);
+  const float2 c2 = make_float2(c, c), M2 = make_float2(-M, -M);
   const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
   for (int v0 = lo + tid; v0 < hi; v0 += U * kTeam) {
     uint4 r[U];
