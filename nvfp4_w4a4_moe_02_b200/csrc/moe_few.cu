@@ -216,7 +216,7 @@ __device__ __forceinline__ void stretch_scale(int e, float* up, float* down) {
 // Stretches of a chunk whose scale is not below kNear of the largest are brought to it by an f16 quotient; the
 // others go in further products of their own, so that an element keeps its 11 bits down to 2^-15 of the largest
 // of its 32.  (Replayed, every chunk with one block far below, or three magnitudes apart: 64 tokens in each of
-// 4 experts of hidden 4096 69.6 -> 84.4 us, 48 skewed of 2048 69.8 -> 81.5; ordinary calls as before, to 0.6 %.)
+// 4 experts of hidden 4096 69.5 -> 84.8 us, 48 skewed of 2048 69.7 -> 81.9; ordinary calls as before, to 0.6 %.)
 constexpr float kNear = 1.220703125e-4f;  // 2^-13
 // The largest scale of a column's chunk, from the two of each lane of the quad.
 __device__ __forceinline__ float quad_max(float2 f) {
@@ -641,7 +641,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) moe_few_stream_kernel(MoeFewAr
                   if (f.x + f.y > 0.0f) {
                     load_b(c, lds16<0>(from), lds16<512>(from), lds16<1024>(from), lds16<1536>(from));
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) c[q] = hmul2(c[q], q < 8 ? q0 : q1);
+                    for (int q = 0; q < 8; ++q) {  // a taken block may hold an infinity
+                      c[q] = q0 != 0 ? hmul2(c[q], q0) : 0u;
+                      c[8 + q] = q1 != 0 ? hmul2(c[8 + q], q1) : 0u;
+                    }
                   }
                   const float e0 = __shfl_sync(0xffffffffu, d, 8 * t), e1 = __shfl_sync(0xffffffffu, d, 8 * t + 4);
                   // the codes are read again, so that nothing is kept in registers for this

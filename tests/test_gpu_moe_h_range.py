@@ -79,3 +79,22 @@ def test_ordinary_tokens_beside_wide_ones(dev):
     got = R.moe_w4a16_layer(x2, logits, 2, pgu, pdn)[0]
     keep = [0, 1, 3, 5]
     assert torch.equal(got[keep], want[keep]) and (got[4] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 9])
+def test_an_infinite_block_beside_finite_ones(dev, T):
+    # the first block of every chunk overflows binary32 and meets positive weights only, its neighbours are far
+    # below: the sum is an infinity, not NaN
+    H, I = 256, 128
+    g = torch.Generator(device=dev)
+    g.manual_seed(7)
+    big = stretch_of(torch.arange(I, device=dev)) % 4 == 0
+    w1 = 0.2 * torch.randn(2, 2, I, H, device=dev, generator=g)
+    w1 = torch.where(big.view(1, 1, I, 1), w1.abs(), w1 * 2.0 ** -12)
+    w2 = 0.05 * torch.randn(2, H, I, device=dev, generator=g)
+    w2[:, :, big] = 0.05
+    x = (2.0 ** 64 * (1.0 + torch.rand(T, H, device=dev, generator=g))).bfloat16()
+    pgu, _ = R.pack_weights(w1.view(2, 2 * I, H).bfloat16(), gate_up_interleave=True)
+    pdn, _ = R.pack_weights(w2.bfloat16())
+    out, ids, w = R.moe_w4a16_layer(x, torch.randn(T, 2, device=dev, generator=g), 2, pgu, pdn)
+    assert (out == float("inf")).all()
