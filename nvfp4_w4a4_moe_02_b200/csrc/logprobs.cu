@@ -634,7 +634,6 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   const uint32_t low = Vec<L>::bound(floor_l);
   const int at_id = (int)id;
   auto element = [&](float l, int v) {
-    if (zero) return 0.0f;
     float g;
     if (exact) {
       const float y = fmaxf((l - st.x) * c, -1000.0f);
@@ -648,7 +647,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   const Span<L> sp(row, (int)a.V, 0, 1);
   if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(grow)) & 15) != 0) {
     const ElementRange r = stretch_elements(a.V, at, stretches);
-    for (auto v = r.first + tid; v < r.end; v += kTeam) Vec<L>::put(grow + v, element(Vec<L>::get(row + v), (int)v));
+    for (auto v = r.first + tid; v < r.end; v += kTeam) Vec<L>::put(grow + v, zero ? 0.0f : element(Vec<L>::get(row + v), (int)v));
     return;
   }
   uint4* gvec = reinterpret_cast<uint4*>(grow + sp.head);
@@ -693,7 +692,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 8 : 4) logprobs_backward_kernel(L
   }
   if (at == 0 && tid < sp.edge) {
     const int v = sp.edge_index(tid);
-    Vec<L>::put(grow + v, element(Vec<L>::get(row + v), v));
+    Vec<L>::put(grow + v, zero ? 0.0f : element(Vec<L>::get(row + v), v));
   }
 }
 
